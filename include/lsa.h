@@ -545,6 +545,96 @@ lsa_status lsa_decode_step(lsa_index* idx, void* latent_K, void* K, void* V,
                            int Hkv, int d, lsa_select_params sp, void* workspace, size_t ws_bytes,
                            void* O, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * KV cache in pages, optionally of 8 bits (this library's own; the method's
+ * pages say only that the KV cache keeps the original representations, "Latent
+ * Sparse Attention: un indice gerarchico per contesti lunghi", paragraph on
+ * retrieval).  The latent keys and the index stay as they are: a selection
+ * lists positions, and the page table says where their keys and values lie.
+ *
+ * Position t of sequence b is slot t % page of the page page_table[b][t / page]:
+ *   K, V        [n_pages][page][Hkv][d]  bf16, or e4m3 codes (1 byte)
+ *   scales      [n_pages][page / 16][2][Hkv] f32 (LSA_KV_E4M3 only): the scale
+ *               of each block of 16 consecutive slots and KV head, keys' then
+ *               values'; the value of a code is code * scale
+ *   page_table  [B][max_pages] int32; entries of pages not in use may hold
+ *               anything outside [0, n_pages), -1 for instance
+ *   status      [8] u32, cleared by the caller before the first call
+ * All of it is device memory of the caller, 16-byte aligned.  page is a power
+ * of two from 16 to 1024, d is 64 or 128, max_pages * page <= 2^31 - 1.
+ * ------------------------------------------------------------------------- */
+typedef enum { LSA_KV_BF16 = 0, LSA_KV_E4M3 = 1 } lsa_kv_format;
+
+typedef struct {
+    void* K;
+    void* V;
+    float* scales;
+    const int32_t* page_table;
+    uint32_t* status;
+    int64_t B;
+    int64_t n_pages;
+    int64_t max_pages;
+    int page;
+    int Hkv;
+    int d;
+    lsa_kv_format format;
+} lsa_paged_kv;
+
+/* Appends the new tokens' keys and values to the pages, rotating keys (and
+ * the same tokens' queries) by position on the way.  Token i < n_new[b] of
+ * sequence b takes position t = start[b] + i.
+ *   k, v     bf16, row b*Nq + i at element offset (b*Nq + i) * k_stride
+ *            (v_stride), Hkv * d contiguous elements; strides are multiples of
+ *            8, so that slices of one fused projection can be passed
+ *   start    [B] int32 positions (>= 0); n_new [B] int32 or NULL (all Nq):
+ *            tokens at and after n_new[b] are padding, neither read nor
+ *            written
+ *   q        bf16 rows of Hq * d at q_stride, or NULL; q_out [B][Nq][Hq][d]
+ *            receives them rotated (q_out == q is allowed when q is
+ *            contiguous); rows of padding are left as they were
+ *   inv_freq [rot_dim / 2] f32 (NULL when rot_dim is 0: no rotation): pair j
+ *            of a head turns by t * inv_freq[j] radians (the product exact to
+ *            about 2^-50 of a turn, whatever t).  The pairs are (j, j +
+ *            rot_dim/2), or (2j, 2j + 1) when interleaved != 0; elements from
+ *            rot_dim on, and V, are not turned.  rot_dim is a multiple of 16
+ *            up to d.
+ * LSA_KV_BF16 rounds each value once.  LSA_KV_E4M3 keeps a power-of-two scale
+ * for each block and head: the smallest 2^k, k >= -64, whose 448-fold reaches
+ * the block's largest finite magnitude among the call's tokens, and not below
+ * the block's scale where the block held earlier tokens of the sequence (slots
+ * before start[b]); those tokens' codes are rounded again when the scale grew
+ * (exact for a power of two, but for codes that become subnormal).  Codes are
+ * rounded to nearest even; infinities become the largest code, NaN stays NaN.
+ * A block's slots after the call's last token are not written; their codes
+ * mean nothing until a token is appended there.
+ * A token whose page is not in [0, n_pages) or whose position is outside
+ * [0, max_pages * page) is left out of the cache and recorded in the status;
+ * a negative start leaves out the whole sequence.  A page that receives tokens
+ * must belong to one sequence of the call.  Asynchronous on `stream`,
+ * graph-capturable, no workspace. */
+lsa_status lsa_paged_append(const lsa_paged_kv* kv, const void* k, int64_t k_stride,
+                            const void* v, int64_t v_stride, const void* q, int64_t q_stride,
+                            void* q_out, int64_t Nq, int Hq, const int32_t* start,
+                            const int32_t* n_new, const float* inv_freq, int rot_dim,
+                            int interleaved, void* stream);
+
+/* lsa_sparse_attn over the paged cache: Q, O [B][Nq][Hq][d] bf16, indices
+ * [B][Nq][s_max] positions (as the selections write them), counts [B][Nq].
+ * fp32 softmax and accumulation; Hq a multiple of Hkv.  A row of count 0 gets
+ * O = 0 and lse = -inf; a listed position outside [0, max_pages * page), or
+ * on a page outside [0, n_pages), is skipped and recorded in the status.  lse
+ * (nullable) [B][Nq][Hq] f32: max + ln(sum) of the scaled logits.  For 8-bit
+ * pages the scales may be any positive numbers.  Asynchronous on `stream`,
+ * graph-capturable, no workspace. */
+lsa_status lsa_paged_attn(const lsa_paged_kv* kv, const void* Q, int64_t Nq, int Hq,
+                          const int32_t* indices, const int32_t* counts, int s_max, float scale,
+                          void* O, float* lse, void* stream);
+
+/* Reads and clears the cache's status word (synchronises `stream`): LSA_OK, or
+ * LSA_ERR_INVALID_ARG when a call since the last check met a position or a
+ * page out of range. */
+lsa_status lsa_paged_check(const lsa_paged_kv* kv, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -24,7 +24,8 @@ __all__ = [
     "lsa_sparse_attn_backward",
     "lsa_prefill_partial_slots", "lsa_prefill_select", "lsa_prefill_attend",
     "lsa_prefill_chunk_host", "lsa_prefill_chunk_queries", "LsaTree", "set_wait_limit",
-    "lsa_decode_workspace_bytes", "lsa_decode_step", "lsa_select_noalloc", "library_path", "kernel_launches", "F32",
+    "lsa_decode_workspace_bytes", "lsa_decode_step", "lsa_select_noalloc",
+    "LsaPagedKV", "lsa_paged_append", "lsa_paged_attn", "library_path", "kernel_launches", "F32",
     "BF16",
 ]
 
@@ -50,6 +51,14 @@ class IndexParams(ctypes.Structure):
 
 class SelectParams(ctypes.Structure):
     _fields_ = [("budget", ctypes.c_int), ("window", ctypes.c_int), ("sinks", ctypes.c_int)]
+
+
+class PagedKV(ctypes.Structure):
+    _fields_ = [("K", ctypes.c_void_p), ("V", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p), ("status", ctypes.c_void_p),
+                ("B", ctypes.c_int64), ("n_pages", ctypes.c_int64), ("max_pages", ctypes.c_int64),
+                ("page", ctypes.c_int), ("Hkv", ctypes.c_int), ("d", ctypes.c_int),
+                ("format", ctypes.c_int)]
 
 
 def _declare(lib):
@@ -99,6 +108,9 @@ def _declare(lib):
                                I),
         "lsa_select_per_key_check": ([P, ctypes.POINTER(I64), P], I),
         "lsa_decode_step": ([P, P, P, P, P, P, P, P, P, P, I, I, I, SelectParams, P, SZ, P, P], I),
+        "lsa_paged_append": ([P, P, I64, P, I64, P, I64, P, I64, I, P, P, P, I, I, P], I),
+        "lsa_paged_attn": ([P, P, I64, I, P, P, I, F, P, P, P], I),
+        "lsa_paged_check": ([P, P], I),
     }
     for name, (args, res) in sigs.items():
         fn = getattr(lib, name)
@@ -637,3 +649,190 @@ def decode_selection_views(workspace, B, s_max):
     indices = workspace[: n_idx * 4].view(torch.int32).view(B, s_max)
     counts = workspace[al: al + B * 4].view(torch.int32).view(B)
     return indices, counts
+
+
+SCALE_BLOCK = 16     # tokens of a page that share an e4m3 scale
+KV_BF16, KV_E4M3 = 0, 1
+
+
+class LsaPagedKV:
+    """A KV cache in pages (C: lsa_paged_kv) over the caller's tensors:
+    k_pages, v_pages [n_pages][page][Hkv][d] (bfloat16, or float8_e4m3fn codes
+    with scales [n_pages][page / 16][2][Hkv] float32) and page_table
+    [B][max_pages] int32.  The tensors are kept and used in place: changing the
+    page table's values moves pages."""
+
+    def __init__(self, k_pages, v_pages, page_table, scales=None):
+        _cuda(k_pages, v_pages, page_table, scales)
+        if k_pages.dtype == torch.bfloat16:
+            fmt = KV_BF16
+        elif k_pages.dtype == torch.float8_e4m3fn:
+            fmt = KV_E4M3
+        else:
+            raise TypeError("pages must be bfloat16 or float8_e4m3fn, got %s" % k_pages.dtype)
+        if k_pages.dim() != 4 or v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype:
+            raise ValueError("k_pages and v_pages must be [n_pages][page][Hkv][d] of one dtype")
+        n_pages, page, Hkv, d = k_pages.shape
+        if page_table.dim() != 2 or page_table.dtype != torch.int32:
+            raise TypeError("page_table must be [B][max_pages] int32")
+        if (scales is not None) != (fmt == KV_E4M3):
+            raise ValueError("8-bit pages have scales, bfloat16 pages none")
+        if scales is not None and (scales.dtype != torch.float32 or tuple(scales.shape) !=
+                                   (n_pages, page // SCALE_BLOCK, 2, Hkv)):
+            raise ValueError("scales must be [n_pages][page / 16][2][Hkv] float32")
+        self.k_pages, self.v_pages = k_pages, v_pages
+        self.page_table, self.scales = page_table, scales
+        self.device = k_pages.device
+        _same_device(self.device, v_pages, page_table, scales)
+        self.status = torch.zeros(8, dtype=torch.int32, device=self.device)
+        # the clearing above is ordered before calls on any stream
+        torch.cuda.current_stream(self.device).synchronize()
+        self.B, self.Hkv, self.d = page_table.shape[0], Hkv, d
+        self._c = PagedKV(k_pages.data_ptr(), v_pages.data_ptr(),
+                          None if scales is None else scales.data_ptr(), page_table.data_ptr(),
+                          self.status.data_ptr(), self.B, n_pages, page_table.shape[1], page, Hkv,
+                          d, fmt)
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def empty(cls, B, n_pages, page, max_pages, Hkv, d, dtype=torch.bfloat16, device="cuda"):
+        """A cache of n_pages unused pages (every page table entry -1)."""
+        shape = (n_pages, page, Hkv, d)
+        k = torch.zeros(shape, dtype=torch.uint8, device=device).view(dtype) \
+            if dtype == torch.float8_e4m3fn else torch.zeros(shape, dtype=dtype, device=device)
+        v = torch.zeros_like(k.view(torch.uint8)).view(dtype)
+        scales = torch.zeros(n_pages, page // SCALE_BLOCK, 2, Hkv, dtype=torch.float32,
+                             device=device) if dtype == torch.float8_e4m3fn else None
+        table = torch.full((B, max_pages), -1, dtype=torch.int32, device=device)
+        return cls(k, v, table, scales)
+
+    def check(self, stream=None):
+        """Raises LsaError if a call since the last check met a position or a page
+        out of range (C: lsa_paged_check)."""
+        with torch.cuda.device(self.device):
+            _check(_lib.lsa_paged_check(self._ref, _stream(stream)))
+
+
+class _on:
+    """Makes `device` (and `stream`, when given) current for a call, so that launches and new
+    tensors belong to them; enters with the stream's handle."""
+
+    def __init__(self, device, stream):
+        self.device, self.stream, self.ctx = device, stream, None
+
+    def __enter__(self):
+        if self.stream is not None:
+            if self.stream.device != self.device:
+                raise ValueError("the stream is on another device")
+            self.ctx = torch.cuda.stream(self.stream)
+        elif torch.cuda.current_device() != self.device.index:
+            self.ctx = torch.cuda.device(self.device)
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return torch.cuda.current_stream(self.device).cuda_stream
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _same_device(device, *ts):
+    for t in ts:
+        if t is not None and t.device != device:
+            raise ValueError("tensors are on different devices (%s, %s)" % (t.device, device))
+
+
+def _int32(device, shape, what, t):
+    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+        raise TypeError("%s must be a contiguous int32 tensor of shape %s" % (what, shape))
+    if t.device != device:
+        raise ValueError("%s is on another device" % what)
+
+
+def _token_stride(t, what, device, B, Nq, d):
+    """Elements between consecutive token rows of a bfloat16 [B][Nq][H][d] tensor whose
+    rows are contiguous (a slice of a wider projection, for instance)."""
+    if t.dtype != torch.bfloat16 or t.device != device or t.dim() != 4:
+        raise TypeError("%s must be a bfloat16 tensor [B][Nq][heads][d] on %s" % (what, device))
+    shape, st = t.shape, t.stride()
+    if shape[0] != B or shape[1] != Nq or shape[3] != d:
+        raise ValueError("%s has shape %s, not [%d][%d][heads][%d]" % (what, tuple(shape), B, Nq, d))
+    if Nq == 0:
+        return shape[2] * d
+    row = st[1] if Nq > 1 else (st[0] if B > 1 else shape[2] * d)
+    if st[3] != 1 or (shape[2] > 1 and st[2] != d) or (B > 1 and st[0] != Nq * row):
+        raise ValueError("%s must have contiguous rows at one distance (strides %s)" % (what, st))
+    return row
+
+
+def lsa_paged_append(cache, k, v, start, n_new=None, q=None, q_out=None, inv_freq=None,
+                     interleaved=False, stream=None):
+    """Appends k, v [B][Nq][Hkv][d] (bfloat16; slices of a fused projection will do) at positions
+    start[b] + i of the paged cache, keys rotated by inv_freq [rot_dim / 2] float32 (None: no
+    rotation); tokens at and after n_new[b] are padding.  With q [B][Nq][Hq][d] the queries are
+    rotated too: into q_out (which may be q; rows of padding are left as they are) or a new
+    tensor, which is returned (None without q).  C: lsa_paged_append."""
+    dev = cache.device
+    B, Nq = k.shape[0], k.shape[1]
+    if B != cache.B or k.shape[2] != cache.Hkv or v.shape[2] != cache.Hkv:
+        raise ValueError("k and v must be [%d][Nq][%d][%d]" % (cache.B, cache.Hkv, cache.d))
+    ks = _token_stride(k, "k", dev, B, Nq, cache.d)
+    vs = _token_stride(v, "v", dev, B, Nq, cache.d)
+    _int32(dev, (B,), "start", start)
+    if n_new is not None:
+        _int32(dev, (B,), "n_new", n_new)
+    rot = 0
+    if inv_freq is not None:
+        if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or inv_freq.device != dev or \
+                not inv_freq.is_contiguous():
+            raise TypeError("inv_freq must be a contiguous 1-D float32 tensor on %s" % dev)
+        rot = 2 * inv_freq.shape[0]
+    qs, Hq = 0, 0
+    with _on(dev, stream) as st:
+        if q is not None:
+            qs, Hq = _token_stride(q, "q", dev, B, Nq, cache.d), q.shape[2]
+            if q_out is None:
+                q_out = torch.empty(B, Nq, Hq, cache.d, dtype=torch.bfloat16, device=dev)
+            elif q_out.shape != q.shape or q_out.dtype != torch.bfloat16 or \
+                    q_out.device != dev or not q_out.is_contiguous():
+                raise ValueError("q_out must be a contiguous bfloat16 tensor of q's shape")
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+        if Nq == 0:
+            return q_out
+        _check(_lib.lsa_paged_append(
+            cache._ref, k.data_ptr(), ks, v.data_ptr(), vs,
+            None if q is None else q.data_ptr(), qs, None if q is None else q_out.data_ptr(), Nq,
+            Hq, start.data_ptr(), None if n_new is None else n_new.data_ptr(),
+            None if inv_freq is None else inv_freq.data_ptr(), rot, int(interleaved), st))
+    return q_out
+
+
+def lsa_paged_attn(cache, Q, indices, counts, scale=None, return_lse=False, out=None,
+                   stream=None):
+    """Attention of Q [B][Nq][Hq][d] (bfloat16) over the listed positions of the paged cache
+    (C: lsa_paged_attn): indices [B][Nq][s_max], counts [B][Nq] int32, as the selections return
+    them.  A row of count 0 gives 0 (lse -inf)."""
+    dev = cache.device
+    if Q.dim() != 4 or Q.dtype != torch.bfloat16 or Q.device != dev or not Q.is_contiguous():
+        raise TypeError("Q must be a contiguous bfloat16 tensor [B][Nq][Hq][d] on %s" % dev)
+    B, Nq, Hq, d = Q.shape
+    if B != cache.B or d != cache.d:
+        raise ValueError("Q must be [%d][Nq][Hq][%d]" % (cache.B, cache.d))
+    s_max = indices.shape[-1]
+    _int32(dev, (B, Nq, s_max), "indices", indices)
+    _int32(dev, (B, Nq), "counts", counts)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if out is not None and (out.shape != Q.shape or out.dtype != torch.bfloat16 or
+                            out.device != dev or not out.is_contiguous()):
+        raise ValueError("out must be a contiguous bfloat16 tensor of Q's shape")
+    with _on(dev, stream) as st:
+        O = out if out is not None else torch.empty_like(Q)
+        lse = torch.empty(B, Nq, Hq, dtype=torch.float32, device=dev) if return_lse else None
+        if Nq == 0:
+            return (O, lse) if return_lse else O
+        _check(_lib.lsa_paged_attn(cache._ref, Q.data_ptr(), Nq, Hq, indices.data_ptr(),
+                                   counts.data_ptr(), s_max, scale, O.data_ptr(),
+                                   None if lse is None else lse.data_ptr(), st))
+    return (O, lse) if return_lse else O

@@ -1253,4 +1253,164 @@ lsa_status lsa_select_noalloc(const lsa_index* idx, const void* latent_Q,
                       sp, DBG_SELECTION, st, "selection");
 }
 
+// ---- paged KV cache -------------------------------------------------------------
+namespace {
+
+lsa_status check_paged(const lsa_paged_kv* kv)
+{
+    if (!kv) return fail(LSA_ERR_INVALID_ARG, "NULL cache");
+    if (!kv->K || !kv->V || !kv->page_table || !kv->status)
+        return fail(LSA_ERR_INVALID_ARG, "NULL cache pointer");
+    if (kv->format != LSA_KV_BF16 && kv->format != LSA_KV_E4M3)
+        return fail(LSA_ERR_INVALID_ARG, "unknown cache format %d", (int)kv->format);
+    if (kv->format == LSA_KV_E4M3 && !kv->scales)
+        return fail(LSA_ERR_INVALID_ARG, "8-bit pages need scales");
+    if (kv->B < 1 || kv->B > 65535)
+        return fail(LSA_ERR_INVALID_ARG, "B=%lld outside [1, 65535]", (long long)kv->B);
+    if (kv->page < 16 || kv->page > 1024 || (kv->page & (kv->page - 1)) != 0)
+        return fail(LSA_ERR_UNSUPPORTED, "page=%d is no power of two from 16 to 1024", kv->page);
+    if (kv->n_pages < 1 || kv->n_pages > 2147483647LL || kv->max_pages < 1 ||
+        kv->max_pages > 2147483647LL / kv->page)
+        return fail(LSA_ERR_INVALID_ARG, "bad page counts (%lld, %lld)", (long long)kv->n_pages,
+                    (long long)kv->max_pages);
+    if (kv->d != 64 && kv->d != 128)
+        return fail(LSA_ERR_UNSUPPORTED, "d=%d not in {64,128}", kv->d);
+    if (kv->Hkv < 1 || kv->Hkv > 1024)
+        return fail(LSA_ERR_INVALID_ARG, "Hkv=%d outside [1, 1024]", kv->Hkv);
+    if (!aligned16(kv->K) || !aligned16(kv->V) || !aligned16(kv->scales) ||
+        !aligned16(kv->page_table) || !aligned16(kv->status))
+        return fail(LSA_ERR_ALIGNMENT, "device pointers must be 16-byte aligned");
+    return LSA_OK;
+}
+
+lsa_status check_paged_heads(const lsa_paged_kv* kv, int Hq)
+{
+    if (Hq < 1 || Hq % kv->Hkv != 0) return fail(LSA_ERR_INVALID_ARG, "Hq %% Hkv != 0");
+    if (Hq > 65536) return fail(LSA_ERR_INVALID_ARG, "Hq=%d > 65536", Hq);
+    return LSA_OK;
+}
+
+lsa_status check_rotation(const lsa_paged_kv* kv, const float* inv_freq, int rot_dim)
+{
+    if (rot_dim < 0 || rot_dim > kv->d || rot_dim % 16 != 0)
+        return fail(LSA_ERR_INVALID_ARG, "rot_dim=%d is no multiple of 16 up to d", rot_dim);
+    if (rot_dim > 0 && !inv_freq) return fail(LSA_ERR_INVALID_ARG, "NULL inv_freq");
+    if (rot_dim > 0 && !aligned16(inv_freq))
+        return fail(LSA_ERR_ALIGNMENT, "device pointers must be 16-byte aligned");
+    return LSA_OK;
+}
+
+lsa_status check_row_stride(int64_t stride, int64_t row, const char* what)
+{
+    if (stride < row || stride > (1LL << 40))
+        return fail(LSA_ERR_INVALID_ARG, "%s_stride=%lld shorter than a row of %lld", what,
+                    (long long)stride, (long long)row);
+    if (stride % 8 != 0)
+        return fail(LSA_ERR_ALIGNMENT, "%s_stride=%lld is no multiple of 8", what,
+                    (long long)stride);
+    return LSA_OK;
+}
+
+}  // namespace
+
+lsa_status lsa_paged_append(const lsa_paged_kv* kv, const void* k, int64_t k_stride,
+                            const void* v, int64_t v_stride, const void* q, int64_t q_stride,
+                            void* q_out, int64_t Nq, int Hq, const int32_t* start,
+                            const int32_t* n_new, const float* inv_freq, int rot_dim,
+                            int interleaved, void* stream)
+{
+    NvtxRange nv("lsa_paged_append");
+    lsa_status s = check_paged(kv);
+    if (s != LSA_OK) return s;
+    if (!k || !v || !start) return fail(LSA_ERR_INVALID_ARG, "NULL argument");
+    if ((q == nullptr) != (q_out == nullptr))
+        return fail(LSA_ERR_INVALID_ARG, "q and q_out go together");
+    if (Nq < 0 || Nq > 2147483647LL / kv->B)
+        return fail(LSA_ERR_INVALID_ARG, "Nq out of range");
+    s = check_rotation(kv, inv_freq, rot_dim);
+    if (s != LSA_OK) return s;
+    const int64_t row = (int64_t)kv->Hkv * kv->d;
+    s = check_row_stride(k_stride, row, "k");
+    if (s == LSA_OK) s = check_row_stride(v_stride, row, "v");
+    if (s == LSA_OK && q) s = check_paged_heads(kv, Hq);
+    if (s == LSA_OK && q) s = check_row_stride(q_stride, (int64_t)Hq * kv->d, "q");
+    if (s != LSA_OK) return s;
+    if (q == q_out && q && q_stride != (int64_t)Hq * kv->d)
+        return fail(LSA_ERR_INVALID_ARG, "q_out == q needs contiguous rows");
+    const void* ptrs[] = {k, v, q, q_out, start, n_new};
+    for (const void* p : ptrs)
+        if (!aligned16(p)) return fail(LSA_ERR_ALIGNMENT, "device pointers must be 16-byte aligned");
+    if (Nq == 0) return LSA_OK;
+    AppendArgs a{};
+    a.k = (const __nv_bfloat16*)k;
+    a.v = (const __nv_bfloat16*)v;
+    a.q = (const __nv_bfloat16*)q;
+    a.q_out = (__nv_bfloat16*)q_out;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.q_stride = q_stride;
+    a.Nq = Nq;
+    a.Hq = q ? Hq : 0;
+    a.start = start;
+    a.n_new = n_new;
+    a.inv_freq = inv_freq;
+    a.rot = rot_dim;
+    a.interleaved = interleaved != 0;
+    const cudaError_t e = launch_paged_append(*kv, a, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "paged append");
+    return LSA_OK;
+}
+
+lsa_status lsa_paged_attn(const lsa_paged_kv* kv, const void* Q, int64_t Nq, int Hq,
+                          const int32_t* indices, const int32_t* counts, int s_max, float scale,
+                          void* O, float* lse, void* stream)
+{
+    NvtxRange nv("lsa_paged_attn");
+    lsa_status s = check_paged(kv);
+    if (s != LSA_OK) return s;
+    if (!Q || !indices || !counts || !O) return fail(LSA_ERR_INVALID_ARG, "NULL argument");
+    if (Nq < 0 || s_max < 1) return fail(LSA_ERR_INVALID_ARG, "bad sizes");
+    s = check_paged_heads(kv, Hq);
+    if (s != LSA_OK) return s;
+    if (Nq > 2147483647LL / (kv->B * Hq))
+        return fail(LSA_ERR_UNSUPPORTED, "too many (query, head) pairs");
+    if (!(scale > 0.f) || isinf(scale))
+        return fail(LSA_ERR_INVALID_ARG, "scale must be finite and > 0");
+    const void* ptrs[] = {Q, indices, counts, O, lse};
+    for (const void* p : ptrs)
+        if (!aligned16(p)) return fail(LSA_ERR_ALIGNMENT, "device pointers must be 16-byte aligned");
+    if (Nq == 0) return LSA_OK;
+    const cudaStream_t st = (cudaStream_t)stream;
+    lsa_select_params none{0, 0, 0};
+    s = dbg_gather(indices, counts, kv->B, Nq, s_max, kv->max_pages * kv->page, PosSrc{nullptr, 0},
+                   none, DBG_BOUNDS, st, "gather indices");
+    if (s != LSA_OK) return s;
+    const cudaError_t e = launch_paged_attn(*kv, Q, Nq, Hq, indices, counts, s_max, scale, O, lse, st);
+    if (e != cudaSuccess) return cuda_fail(e, "paged attention");
+    return LSA_OK;
+}
+
+lsa_status lsa_paged_check(const lsa_paged_kv* kv, void* stream)
+{
+    lsa_status s = check_paged(kv);
+    if (s != LSA_OK) return s;
+    cudaStream_t st = (cudaStream_t)stream;
+    uint32_t h[8] = {0};
+    cudaError_t e = cudaMemcpyAsync(h, kv->status, sizeof(h), cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    if (e == cudaSuccess) e = cudaMemsetAsync(kv->status, 0, sizeof(h), st);
+    if (e != cudaSuccess) return cuda_fail(e, "cache check");
+    switch (h[0]) {
+    case DEV_OK: return LSA_OK;
+    case DEV_BAD_INDEX:
+        return fail(LSA_ERR_INVALID_ARG, "a listed position (%d) was outside the page table",
+                    (int)h[2]);
+    case DEV_BAD_PAGE:
+        return fail(LSA_ERR_INVALID_ARG,
+                    "a position (%d) outside the page table, or on a page outside the pool",
+                    (int)h[2]);
+    default: return fail(LSA_ERR_INTERNAL, "device status %u (detail %u)", h[0], h[2]);
+    }
+}
+
 }  // extern "C"

@@ -1,0 +1,60 @@
+// paged.cuh -- device helpers of the paged KV cache's kernels.
+#pragma once
+
+#include "lsa_internal.cuh"
+
+namespace lsa {
+
+// The page that holds position t of sequence b, or -1 (recorded) when the
+// position is outside the table or the page outside the pool.
+__device__ __forceinline__ int32_t page_of(const lsa_paged_kv& kv, int64_t b, int64_t t)
+{
+    int32_t pg = -1;
+    if (t >= 0 && t < kv.max_pages * kv.page) {
+        pg = kv.page_table[b * kv.max_pages + t / kv.page];
+        if (pg < 0 || pg >= kv.n_pages) pg = -1;
+    }
+    if (pg < 0) dev_error(kv.status, DEV_BAD_PAGE, (uint32_t)t);
+    return pg;
+}
+
+// Smallest power of two 2^k, k >= -64, with amax <= 448 * 2^k (448 = 0.875 * 2^9).
+__device__ __forceinline__ float e4m3_scale(float amax)
+{
+    const uint32_t u = __float_as_uint(amax);
+    int k = (int)(u >> 23) - 126 - 9 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+    if (k < -64) k = -64;
+    return __uint_as_float((uint32_t)(k + 127) << 23);
+}
+
+// Magnitude of a finite value, 0 for infinities and NaN.
+__device__ __forceinline__ float finite_abs(float x)
+{
+    const float a = fabsf(x);
+    return a <= 3.402823466e38f ? a : 0.f;
+}
+
+// Two codes (lo in the low byte), rounded to nearest even; infinities give the
+// largest code, NaN stays NaN.
+__device__ __forceinline__ uint16_t e4m3x2(float lo, float hi)
+{
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// The values of two codes as f16 (exact).
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint16_t c)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
+    return r;
+}
+
+__device__ __forceinline__ float e4m3_value(uint8_t c)
+{
+    const uint32_t r = e4m3x2_f16x2((uint16_t)c);
+    return __half2float(__ushort_as_half((unsigned short)(r & 0xffffu)));
+}
+
+}  // namespace lsa

@@ -1,0 +1,548 @@
+"""The paged KV cache on the GPU against binary64 (tests/paged_plain.py).
+
+Tolerances, from the roundings each result passes (eps/2 relative: bf16 2^-8,
+fp16 2^-11, e4m3 2^-4 or half its spacing):
+  rotation     cos, sin and the two products in fp32: 2^-21 (|x| + |y|) of a pair;
+  bf16 pages   one rounding more: 2^-8 of the value;
+  8-bit pages  a code is within half the grid's spacing (at the value, over the
+               scale) of the rotated value plus the rotation's error; the scale is
+               that of a largest magnitude off by the rotation's error at most;
+  attention    logits in fp32 over d products: dz = 2^-18 of the largest sum of
+               |q k|; weights rounded to fp16 at least, 2^-11, and exp, sum and
+               rescaling in fp32: (2^-10 + 4 dz) sum p |v|; output 2^-8 |o| in bf16;
+               lse 2 dz + 2^-19 (1 + |lse|).
+"""
+import numpy as np
+import pytest
+import torch
+
+import paged_plain as plain
+
+pytestmark = pytest.mark.gpu
+
+lsa = pytest.importorskip("long_context_indexing_b200")
+
+FP8 = torch.float8_e4m3fn
+
+
+def _freq(rot):
+    return (1e6 ** (-np.arange(0, rot, 2) / max(rot, 1))).astype(np.float32)
+
+
+def _cache(rng, B, Hkv, d, page, max_pages, dtype, spare=2):
+    """A cache of random values whose page table is a random permutation."""
+    n = B * max_pages + spare
+    table = rng.permutation(n)[:B * max_pages].reshape(B, max_pages).astype(np.int32)
+    K = torch.from_numpy(rng.standard_normal((n, page, Hkv, d)).astype(np.float32))
+    V = torch.from_numpy(rng.standard_normal((n, page, Hkv, d)).astype(np.float32))
+    scales = None
+    if dtype == FP8:
+        K, V = (K * 96).clamp(-448, 448), (V * 96).clamp(-448, 448)
+        e = rng.integers(-9, -5, (n, page // 16, 2, Hkv))
+        scales = torch.from_numpy(np.exp2(e).astype(np.float32)).cuda()
+    return lsa.LsaPagedKV(K.to(dtype).cuda(), V.to(dtype).cuda(), torch.from_numpy(table).cuda(),
+                          scales)
+
+
+def _state(c):
+    """The cache as numpy binary64: codes (or bf16 values), scales, table."""
+    return dict(K=c.k_pages.float().cpu().double().numpy(),
+                V=c.v_pages.float().cpu().double().numpy(),
+                scales=None if c.scales is None else c.scales.cpu().double().numpy(),
+                table=c.page_table.cpu().numpy())
+
+
+def _values(st):
+    if st["scales"] is None:
+        return st["K"], st["V"]
+    s = np.repeat(st["scales"], plain.BLOCK, axis=1)          # [n_pages][page][2][Hkv]
+    return st["K"] * s[:, :, 0, :, None], st["V"] * s[:, :, 1, :, None]
+
+
+def _new(rng, B, Nq, H, d):
+    """Tokens whose norms spread over a factor of 64, rounded to bf16."""
+    x = rng.standard_normal((B, Nq, H, d)) * np.exp2(rng.uniform(-3, 3, (B, Nq, 1, 1)))
+    return torch.from_numpy(x.astype(np.float32)).to(torch.bfloat16)
+
+
+def _pair_sum(x, rot, inter):
+    """|x| + |y| of each element's pair."""
+    a = np.abs(x).copy()
+    r = a[..., :rot].copy()
+    if inter:
+        o = r.reshape(r.shape[:-1] + (-1, 2))[..., ::-1].reshape(r.shape)
+    else:
+        o = np.concatenate([r[..., rot // 2:], r[..., :rot // 2]], -1)
+    a[..., :rot] = r + o
+    return a
+
+
+def _check_append(c, before, args, got_q=None, q_before=None):
+    """The cache after an append against binary64 from its state before."""
+    k, v, start, n_new, inv, inter, q = args
+    kd, vd = k.float().double().numpy(), v.float().double().numpy()
+    qd = None if q is None else q.float().double().numpy()
+    want = {n: (None if x is None else x.copy()) for n, x in before.items()}
+    wq = plain.append(want, kd, vd, start, n_new, inv, inter, qd)
+    got = _state(c)
+    rot = 2 * len(inv)
+    err = np.zeros_like(want["K"])          # the rotation's error where a key was written
+    touched = np.zeros(want["K"].shape[:2], bool)
+    page = want["K"].shape[1]
+    pair = _pair_sum(kd, rot, inter)
+    written = {n: np.full_like(want["K"], np.nan) for n in "KV"}
+    for b in range(kd.shape[0]):
+        for i in range(min(n_new[b], kd.shape[1])):
+            t = int(start[b]) + i
+            if start[b] < 0 or t // page >= want["table"].shape[1]:
+                continue
+            pg = want["table"][b, t // page]
+            if pg < 0 or pg >= want["K"].shape[0]:
+                continue
+            err[pg, t % page] = 2.0 ** -21 * pair[b, i]
+            written["K"][pg, t % page] = plain.rotate(kd[b, i], t, inv, inter)
+            written["V"][pg, t % page] = vd[b, i]
+            touched[pg, t % page] = True
+    for j, n in enumerate("KV"):
+        e = err if n == "K" else 0.0 * err
+        if want["scales"] is None:
+            bad = np.abs(got[n] - want[n]) > np.where(touched[..., None, None],
+                                                      2.0 ** -8 * np.abs(want[n]) + 1.01 * e, 0.0)
+            assert not bad.any(), (n, np.argwhere(bad)[:3])
+            continue
+        # scales equal, or those of a maximum off by the rotation's error
+        gs, ws = got["scales"][:, :, j], want["scales"][:, :, j]
+        if n == "V":
+            assert np.array_equal(gs, ws)
+        else:
+            for at in np.argwhere(gs != ws):
+                pg, blk, h = at
+                w = written[n][pg, blk * 16:(blk + 1) * 16, h]
+                m, tol = np.nanmax(np.abs(w)), np.nanmax(err[pg, blk * 16:(blk + 1) * 16, h])
+                assert gs[tuple(at)] in (plain.block_scale(m - tol), plain.block_scale(m + tol))
+        s = np.repeat(gs, plain.BLOCK, axis=1)[..., None]
+        x = written[n]
+        step = plain.half_step(np.where(np.isfinite(x), x, 0) / np.where(s > 0, s, 1))
+        bad = touched[..., None, None] & np.isfinite(x) & (
+            np.abs(got[n] * s - x) > s * step * 1.0001 + 1.01 * e)
+        assert not bad.any(), (n, np.argwhere(bad)[:3], got[n][bad][:3], x[bad][:3])
+        same = np.broadcast_to(gs == ws, gs.shape)
+        rest = ~touched[..., None, None] & np.repeat(same, plain.BLOCK, axis=1)[..., None]
+        rest = np.broadcast_to(rest, got[n].shape)
+        assert np.array_equal(got[n][rest], want[n][rest], equal_nan=True), n
+    if q is not None:
+        g = got_q.float().cpu().double().numpy()
+        live = ~np.isnan(wq).all(axis=(2, 3))
+        tol = 2.0 ** -8 * np.abs(wq) + 1.01 * 2.0 ** -21 * _pair_sum(qd, rot, inter)
+        assert (np.abs(g - wq)[live] <= tol[live]).all()
+        if q_before is not None:
+            old = q_before.float().cpu().double().numpy()
+            assert np.array_equal(g[~live], old[~live])
+
+
+APPEND = [
+    # B, Nq, Hq, Hkv, d, page, rot, inter, start
+    (1, 1, 8, 1, 128, 16, 128, False, 0),
+    (3, 1, 32, 4, 128, 64, 128, False, 37),
+    (2, 17, 6, 2, 64, 16, 64, True, 15),
+    (1, 100, 24, 3, 128, 32, 64, False, 1),
+    (4, 33, 8, 8, 64, 128, 32, True, 63),
+    (2, 48, 4, 4, 128, 16, 16, False, 16),
+    (1, 5, 16, 16, 64, 1024, 0, False, 9),
+]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, FP8])
+@pytest.mark.parametrize("B,Nq,Hq,Hkv,d,page,rot,inter,start", APPEND)
+def test_append(dtype, B, Nq, Hq, Hkv, d, page, rot, inter, start):
+    rng = np.random.default_rng(Nq * 131 + d + rot)
+    c = _cache(rng, B, Hkv, d, page, (start + B * 5 + Nq) // page + 1, dtype)
+    k, v, q = _new(rng, B, Nq, Hkv, d), _new(rng, B, Nq, Hkv, d), _new(rng, B, Nq, Hq, d)
+    st = np.array([start + 5 * b for b in range(B)], np.int32)
+    inv = _freq(rot)
+    before = _state(c)
+    out = lsa.lsa_paged_append(c, k.cuda(), v.cuda(), torch.from_numpy(st).cuda(), q=q.cuda(),
+                               inv_freq=torch.from_numpy(inv).cuda() if rot else None,
+                               interleaved=inter)
+    c.check()
+    _check_append(c, before, (k, v, st, [Nq] * B, inv, inter, q), out)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, FP8])
+def test_append_padded_batch_from_fused_slices(dtype):
+    # unequal lengths with empty and overlong counts; k, v, q sliced from one projection;
+    # padding rows hold NaN and are neither read nor written
+    rng = np.random.default_rng(3)
+    B, Nq, Hq, Hkv, d, page = 5, 40, 8, 2, 128, 32
+    c = _cache(rng, B, Hkv, d, page, 4, dtype)
+    qkv = _new(rng, B, Nq, Hq + 2 * Hkv, d)
+    n_new = np.array([40, 0, 1, 23, 99], np.int32)
+    for b in range(B):
+        qkv[b, n_new[b]:] = float("nan")
+    q, k, v = qkv.split([Hq, Hkv, Hkv], 2)
+    dq, dk, dv = qkv.cuda().split([Hq, Hkv, Hkv], 2)
+    start = np.array([0, 50, 77, 30, 81], np.int32)
+    inv = _freq(128)
+    before = _state(c)
+    q_out = torch.full((B, Nq, Hq, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    q0 = q_out.clone()
+    r = lsa.lsa_paged_append(c, dk, dv, torch.from_numpy(start).cuda(),
+                             n_new=torch.from_numpy(n_new).cuda(), q=dq, q_out=q_out,
+                             inv_freq=torch.from_numpy(inv).cuda())
+    assert r is q_out
+    c.check()
+    _check_append(c, before, (k, v, start, n_new.tolist(), inv, False, q), q_out, q0)
+
+
+def test_append_token_by_token_grows_scales():
+    # one token a call with norms that rise and fall by up to 2^9: every step against
+    # binary64 from the step before, among them blocks of zeros, then of tiny values
+    rng = np.random.default_rng(11)
+    B, Hkv, d, page = 2, 2, 64, 16
+    c = lsa.LsaPagedKV.empty(B, 6, page, 3, Hkv, d, FP8)
+    c.page_table.copy_(torch.tensor([[4, 0, 2], [1, 5, 3]], dtype=torch.int32))
+    inv = _freq(64)
+    dinv = torch.from_numpy(inv).cuda()
+    for t in range(40):
+        size = [0.0, 2.0 ** -30, 2.0 ** rng.uniform(-4, 5), 2.0 ** rng.uniform(-4, 5)][rng.integers(4)]
+        k = (_new(rng, B, 1, Hkv, d).float() * size).to(torch.bfloat16)
+        v = (_new(rng, B, 1, Hkv, d).float() * size).to(torch.bfloat16)
+        st = np.full(B, t, np.int32)
+        before = _state(c)
+        lsa.lsa_paged_append(c, k.cuda(), v.cuda(), torch.from_numpy(st).cuda(), inv_freq=dinv)
+        _check_append(c, before, (k, v, st, [1] * B, inv, False, None))
+    c.check()
+
+
+def test_append_non_finite_values():
+    # infinities take the largest code and do not enter the scale; NaN stays NaN
+    rng = np.random.default_rng(5)
+    c = lsa.LsaPagedKV.empty(1, 1, 16, 1, 1, 64, FP8)
+    k, v = _new(rng, 1, 16, 1, 64), _new(rng, 1, 16, 1, 64)
+    v[0, 3, 0, 5], v[0, 4, 0, 6], v[0, 5, 0, 7] = float("inf"), float("-inf"), float("nan")
+    c.page_table.zero_()
+    lsa.lsa_paged_append(c, k.cuda(), v.cuda(), torch.zeros(1, dtype=torch.int32, device="cuda"))
+    fin = v.float()[torch.isfinite(v.float())].abs().max().item()
+    assert c.scales[0, 0, 1, 0].item() == plain.block_scale(fin)
+    got = c.v_pages.float().cpu()[0, :, 0]
+    assert got[3, 5] == 448 and got[4, 6] == -448 and torch.isnan(got[5, 7])
+    assert torch.isfinite(got).sum() == 16 * 64 - 1
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, FP8])
+def test_append_out_of_range_is_left_out_and_recorded(dtype):
+    rng = np.random.default_rng(8)
+    B, Nq, Hkv, d, page = 5, 20, 2, 64, 16
+    c = _cache(rng, B, Hkv, d, page, 4, dtype)
+    table = c.page_table
+    table[0, 1], table[1, 1] = -1, 10 ** 6          # no page; a page outside the pool
+    start = np.array([0, 10, -3, 2 ** 31 - 10, 55], np.int32)    # 55: runs past the table
+    k, v = _new(rng, B, Nq, Hkv, d), _new(rng, B, Nq, Hkv, d)
+    before = _state(c)
+    lsa.lsa_paged_append(c, k.cuda(), v.cuda(), torch.from_numpy(start).cuda())
+    with pytest.raises(lsa.LsaError) as e:
+        c.check()
+    assert e.value.code == 1
+    c.check()                                       # the status was cleared
+    _check_append(c, before, (k, v, start, [Nq] * B, _freq(0), False, None))
+
+
+def test_append_rotates_far_positions_and_in_place():
+    # positions up to 2^31 - 1: angles far past what 32 bits hold; q_out is q itself
+    rng = np.random.default_rng(9)
+    d, page = 128, 1024
+    far = np.array([10485759, 2 ** 27 + 1, 2 ** 31 - 1025], np.int32)
+    B = len(far)
+    table = torch.full((B, (2 ** 31 - 1) // page), -1, dtype=torch.int32, device="cuda")
+    for b in range(B):
+        table[b, far[b] // page] = b
+    pages = torch.zeros(B, page, 1, d, dtype=torch.bfloat16, device="cuda")
+    c = lsa.LsaPagedKV(pages, pages.clone(), table)
+    k, q = _new(rng, B, 1, 1, d), _new(rng, B, 1, 2, d)
+    inv = _freq(128)
+    dq = q.cuda()
+    out = lsa.lsa_paged_append(c, k.cuda(), k.cuda(), torch.from_numpy(far).cuda(), q=dq, q_out=dq,
+                               inv_freq=torch.from_numpy(inv).cuda())
+    c.check()
+    assert out is dq
+    for b in range(B):
+        for x, y in ((q[b, 0], dq[b, 0]), (k[b, 0], c.k_pages[b, far[b] % page])):
+            want = plain.rotate(x.float().numpy(), far[b], inv, False)
+            got = y.float().cpu().double().numpy()
+            tol = 2.0 ** -8 * np.abs(want) + 2.0 ** -21 * _pair_sum(x.float().double().numpy(), d, False)
+            assert (np.abs(got - want) <= 1.01 * tol).all()
+
+
+# ---- attention ----------------------------------------------------------------------------------
+
+def _check_attn(c, Q, idx, cnt, scale, O, lse):
+    Kv, Vv = _values(_state(c))
+    Qd = Q.float().cpu().double().numpy()
+    ro, ra, rz, rl = plain.attend(Kv, Vv, c.page_table.cpu().numpy(), Qd, idx, cnt, scale)
+    dz = 2.0 ** -18 * rz
+    tol = 2.0 ** -8 * np.abs(ro) + (2.0 ** -10 + 4 * dz)[..., None] * ra + 1e-38
+    go = O.float().cpu().double().numpy()
+    assert (np.abs(go - ro) <= tol).all(), np.max(np.abs(go - ro) / tol)
+    gl = lse.cpu().double().numpy()
+    empty = np.isneginf(rl)
+    assert np.array_equal(np.isneginf(gl), empty)
+    ok = np.abs(gl - np.where(empty, 0, rl))[~empty] <= \
+        (2 * dz + 2.0 ** -19 * (1 + np.abs(rl)))[~empty]
+    assert ok.all()
+
+
+def _rows(rng, B, Nq, T, s_max, counts):
+    idx = np.full((B, Nq, s_max), -1, np.int32)
+    cnt = np.zeros((B, Nq), np.int32)
+    for r in range(B * Nq):
+        n = counts[r % len(counts)]
+        cnt[r // Nq, r % Nq] = n
+        idx[r // Nq, r % Nq, :n] = rng.choice(T, n, replace=n > T)
+    return idx, cnt
+
+
+ATTN = [
+    # B, Nq, Hq, Hkv, d, page, max_pages, s_max, counts
+    (1, 1, 8, 1, 128, 16, 4, 40, [40]),
+    (2, 3, 32, 4, 128, 64, 3, 170, [170, 1, 0, 33, 64, 15]),
+    (3, 5, 24, 8, 64, 32, 4, 100, [100, 99, 0, 2, 17]),
+    (1, 4, 5, 1, 64, 16, 9, 31, [31, 16, 7, 0]),
+    (2, 1, 16, 1, 128, 128, 1, 128, [128, 127]),
+    (1, 2, 2, 2, 64, 1024, 1, 700, [700, 513]),
+    (4, 1, 28, 4, 128, 16, 40, 640, [640, 0, 639, 333]),
+    (1, 1, 32, 4, 128, 64, 80, 5000, [5000]),
+    (2, 40, 6, 3, 128, 32, 2, 1, [1, 0]),
+    (1, 1, 80, 1, 64, 16, 4, 64, [50]),
+]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, FP8])
+@pytest.mark.parametrize("B,Nq,Hq,Hkv,d,page,max_pages,s_max,counts", ATTN)
+def test_attention(dtype, B, Nq, Hq, Hkv, d, page, max_pages, s_max, counts):
+    rng = np.random.default_rng(Hq * 17 + s_max)
+    c = _cache(rng, B, Hkv, d, page, max_pages, dtype)
+    idx, cnt = _rows(rng, B, Nq, max_pages * page, s_max, counts)
+    Q = torch.from_numpy((rng.standard_normal((B, Nq, Hq, d)) * 2).astype(np.float32)).to(torch.bfloat16)
+    O, lse = lsa.lsa_paged_attn(c, Q.cuda(), torch.from_numpy(idx).cuda(),
+                                torch.from_numpy(cnt).cuda(), return_lse=True)
+    c.check()
+    _check_attn(c, Q, idx, cnt, 1 / np.sqrt(d), O, lse)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, FP8])
+def test_attention_never_reads_unlisted_slots(dtype):
+    # every slot that no row lists holds NaN, every scale of a block without a listed
+    # slot too; indices behind a row's count are garbage
+    rng = np.random.default_rng(21)
+    B, Nq, Hq, Hkv, d, page, mp, s = 2, 3, 16, 2, 128, 32, 6, 50
+    c = _cache(rng, B, Hkv, d, page, mp, dtype)
+    idx, cnt = _rows(rng, B, Nq, mp * page, s, [50, 13, 0, 1, 37, 16])
+    keep = np.zeros((c.k_pages.shape[0], page), bool)
+    table = c.page_table.cpu().numpy()
+    for b in range(B):
+        for i in range(Nq):
+            t = idx[b, i, :cnt[b, i]]
+            keep[table[b, t // page], t % page] = True
+            idx[b, i, cnt[b, i]:] = rng.integers(-5, 10 ** 9, s - cnt[b, i])
+    gone = torch.from_numpy(~keep).cuda()
+    for x in (c.k_pages, c.v_pages):
+        if dtype == FP8:
+            x.view(torch.uint8)[gone] = 0x7F
+        else:
+            x[gone] = float("nan")
+    if dtype == FP8:
+        dead = ~keep.reshape(-1, page // 16, 16).any(-1)
+        c.scales[torch.from_numpy(dead).cuda()] = float("nan")
+    Q = _new(rng, B, Nq, Hq, d)
+    O, lse = lsa.lsa_paged_attn(c, Q.cuda(), torch.from_numpy(idx).cuda(),
+                                torch.from_numpy(cnt).cuda(), return_lse=True)
+    c.check()
+    st = _state(c)
+    st["K"], st["V"] = np.nan_to_num(st["K"]), np.nan_to_num(st["V"])
+    if st["scales"] is not None:
+        st["scales"] = np.nan_to_num(st["scales"])
+    Kv, Vv = _values(st)
+    ro, ra, rz, rl = plain.attend(Kv, Vv, table, Q.float().double().numpy(), idx, cnt, 1 / np.sqrt(d))
+    go = O.float().cpu().double().numpy()
+    dz = 2.0 ** -18 * rz
+    assert (np.abs(go - ro) <= 2.0 ** -8 * np.abs(ro) + (2.0 ** -10 + 4 * dz)[..., None] * ra).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, FP8])
+def test_attention_skips_and_records_bad_positions(dtype):
+    rng = np.random.default_rng(22)
+    B, Nq, Hq, Hkv, d, page, mp, s = 2, 2, 8, 2, 64, 16, 8, 90
+    c = _cache(rng, B, Hkv, d, page, mp, dtype)
+    idx, cnt = _rows(rng, B, Nq, mp * page, s, [90, 90, 60, 3])
+    Q = _new(rng, B, Nq, Hq, d)
+    idx[0, 0, 5], idx[0, 0, 40], idx[1, 0, 7] = -1, mp * page, 2 ** 31 - 1
+    idx[1, 1, :3] = 3                                 # the whole row on a page that is gone
+    c.page_table[1, 0] = -1
+    c.page_table[0, 2] = c.k_pages.shape[0]
+    O, lse = lsa.lsa_paged_attn(c, Q.cuda(), torch.from_numpy(idx).cuda(),
+                                torch.from_numpy(cnt).cuda(), return_lse=True)
+    with pytest.raises(lsa.LsaError) as e:
+        c.check()
+    assert e.value.code == 1
+    c.check()
+    _check_attn(c, Q, idx, cnt, 1 / np.sqrt(d), O, lse)
+    assert (O[1, 1] == 0).all() and torch.isneginf(lse[1, 1]).all()
+
+
+def test_attention_extreme_logits_and_scales():
+    # logits of a few thousand with one key far above the others; V scales 2^20 apart
+    # between blocks; K of zeros; any positive scales, powers of two or not
+    rng = np.random.default_rng(23)
+    B, Nq, Hq, Hkv, d, page, mp, s = 1, 4, 8, 1, 128, 64, 8, 500
+    c = _cache(rng, B, Hkv, d, page, mp, FP8)
+    sc = np.exp2(rng.uniform(-12, -6, c.scales.shape)).astype(np.float32)
+    sc[:, ::2, 1] *= 2.0 ** 20
+    c.scales.copy_(torch.from_numpy(sc))
+    c.k_pages.view(torch.uint8)[c.page_table[0, 3].item()] = 0
+    idx, cnt = _rows(rng, B, Nq, mp * page, s, [500, 400, 300, 2])
+    Q = _new(rng, B, Nq, Hq, d).float()
+    Q[0, 1] *= 100
+    Q[0, 2, ::2] *= 1e4
+    Q[0, 2, 1] = 0
+    Q[0, 3] *= 1e-6
+    Q = Q.to(torch.bfloat16)
+    O, lse = lsa.lsa_paged_attn(c, Q.cuda(), torch.from_numpy(idx).cuda(),
+                                torch.from_numpy(cnt).cuda(), return_lse=True)
+    c.check()
+    _check_attn(c, Q, idx, cnt, 1 / np.sqrt(d), O, lse)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, FP8])
+def test_pages_past_32_bits(dtype):
+    # a pool of over 2^32 bytes for each of K and V; the pages in use lie at its end
+    page, Hkv, d = 1024, 8, 128
+    bytes_page = page * Hkv * d * (1 if dtype == FP8 else 2)
+    n = 2 ** 32 // bytes_page + 9
+    k = torch.empty(n, page, Hkv, d, dtype=torch.uint8 if dtype == FP8 else dtype, device="cuda")
+    v = torch.empty_like(k)
+    k, v = (k.view(FP8), v.view(FP8)) if dtype == FP8 else (k, v)
+    scales = torch.ones(n, page // 16, 2, Hkv, device="cuda") if dtype == FP8 else None
+    table = torch.tensor([[n - 1, n - 3]], dtype=torch.int32, device="cuda")
+    c = lsa.LsaPagedKV(k, v, table, scales)
+    rng = np.random.default_rng(31)
+    N = 2000
+    kn, vn = _new(rng, 1, N, Hkv, d), _new(rng, 1, N, Hkv, d)
+    lsa.lsa_paged_append(c, kn.cuda(), vn.cuda(), torch.zeros(1, dtype=torch.int32, device="cuda"))
+    idx = rng.permutation(N)[None, None, :300].astype(np.int32)
+    cnt = np.array([[300]], np.int32)
+    Q = _new(rng, 1, 1, 16, d)
+    O, lse = lsa.lsa_paged_attn(c, Q.cuda(), torch.from_numpy(idx).cuda(),
+                                torch.from_numpy(cnt).cuda(), return_lse=True)
+    c.check()
+    small = lsa.LsaPagedKV(k[-3:].clone(), v[-3:].clone(),
+                           torch.tensor([[2, 0]], dtype=torch.int32, device="cuda"),
+                           None if scales is None else scales[-3:].clone())
+    _check_attn(small, Q, idx, cnt, 1 / np.sqrt(d), O, lse)
+
+
+def test_streams_graphs_and_two_calls_at_once():
+    # the same append and attention eagerly, on a side stream, captured and replayed, and
+    # two at once on two streams over two caches give the same bits
+    rng = np.random.default_rng(41)
+    B, Hq, Hkv, d, page, mp, s = 4, 32, 4, 128, 64, 8, 300
+    base = _cache(rng, B, Hkv, d, page, mp, FP8)
+
+    def copy():
+        return lsa.LsaPagedKV(base.k_pages.clone(), base.v_pages.clone(), base.page_table.clone(),
+                              base.scales.clone())
+
+    k, v, q = (_new(rng, B, 3, h, d).cuda() for h in (Hkv, Hkv, Hq))
+    start = torch.tensor([5, 60, 333, 509], dtype=torch.int32, device="cuda")
+    inv = torch.from_numpy(_freq(128)).cuda()
+    idx, cnt = (torch.from_numpy(x).cuda() for x in _rows(rng, B, 3, mp * page, s, [300, 17, 250]))
+
+    def both(c, stream=None):
+        qr = lsa.lsa_paged_append(c, k, v, start, q=q, inv_freq=inv, stream=stream)
+        return lsa.lsa_paged_attn(c, qr, idx, cnt, return_lse=True, stream=stream)
+
+    c0 = copy()
+    O0, l0 = both(c0)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    ca, cb = copy(), copy()
+    torch.cuda.synchronize()
+    (Oa, la), (Ob, lb) = both(ca, s1), both(cb, s2)
+    torch.cuda.synchronize()
+    for c, O, l in ((ca, Oa, la), (cb, Ob, lb)):
+        assert torch.equal(O, O0) and torch.equal(l, l0)
+        assert torch.equal(c.k_pages.view(torch.uint8), c0.k_pages.view(torch.uint8))
+        assert torch.equal(c.scales, c0.scales)
+    cg = copy()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        Og, lg = both(cg)
+    for _ in range(3):
+        Og.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(Og, O0) and torch.equal(lg, l0)
+    cg.check()
+    assert torch.equal(cg.v_pages.view(torch.uint8), c0.v_pages.view(torch.uint8))
+
+
+def test_run_together_with_the_retrieval():
+    # chunk by chunk: tokens into pages, latents into the index, the retrieval's selection,
+    # attention through the page table; bf16 pages give what lsa_sparse_attn gives over a
+    # contiguous cache, 8-bit pages the binary64 attention over their values
+    import synth
+    w = synth.workload("128k", T=8192, nq=256, M=64, R=512, W=64, S=4)
+    inp = synth.prefill_inputs(w, 3, "cpu")
+    dev = {n: x.cuda() for n, x in inp.items()}
+    span, page = w.p * w.G, 64
+    idx = lsa.LsaIndex(1, w.T, w.p, w.G, w.k, w.L, lsa.BF16)
+    idx.build(dev["latent_K"], (w.T // span) * span)
+    sel, cnt = lsa.lsa_select(idx, dev["latent_Q"], dev["positions"].int(), w.R, w.W, w.S)
+    want = lsa.lsa_sparse_attn(dev["Q"], dev["K"], dev["V"], sel, cnt)
+    rng = np.random.default_rng(1)
+    for dtype in (torch.bfloat16, FP8):
+        c = lsa.LsaPagedKV.empty(1, w.T // page, page, w.T // page, w.Hkv, w.d, dtype)
+        c.page_table.copy_(torch.from_numpy(rng.permutation(w.T // page).astype(np.int32))[None])
+        for t in range(0, w.T, 1000):           # chunks that end inside blocks and pages
+            e = min(t + 1000, w.T)
+            lsa.lsa_paged_append(c, dev["K"][:, t:e].contiguous(), dev["V"][:, t:e].contiguous(),
+                                 torch.tensor([t], dtype=torch.int32, device="cuda"))
+        O, lse = lsa.lsa_paged_attn(c, dev["Q"], sel, cnt, return_lse=True)
+        c.check()
+        if dtype == torch.bfloat16:
+            assert (O.float() - want.float()).abs().max() <= 2e-2
+        r = np.arange(0, w.nq, 37)
+        _check_attn(c, inp["Q"][:, r], sel.cpu().numpy()[:, r], cnt.cpu().numpy()[:, r],
+                    1 / np.sqrt(w.d), O[:, r], lse[:, r])
+
+
+def test_wrong_tensors_are_refused():
+    # tensors of wrong shape, type or place are refused before any launch
+    c = lsa.LsaPagedKV.empty(2, 4, 16, 2, 2, 64)
+    k = torch.zeros(2, 3, 2, 64, dtype=torch.bfloat16, device="cuda")
+    st = torch.zeros(2, dtype=torch.int32, device="cuda")
+    n0 = lsa.kernel_launches()
+    for bad in (dict(k=k[:1]), dict(k=k.float()), dict(k=k.cpu()), dict(k=k[..., :32]),
+                dict(v=k[:, :2]), dict(v=k.transpose(1, 2)), dict(start=st.long()),
+                dict(start=st[:1]), dict(n_new=st[:1]), dict(inv_freq=st),
+                dict(inv_freq=torch.zeros(5, device="cuda")), dict(q_out=k),
+                dict(q=k[:, :, :1]), dict(k=k[:, :, :1])):
+        args = dict(k=k, v=k, start=st)
+        args.update(bad)
+        with pytest.raises((ValueError, TypeError, lsa.LsaError)):
+            lsa.lsa_paged_append(c, args.pop("k"), args.pop("v"), args.pop("start"), **args)
+    Q = torch.zeros(2, 3, 4, 64, dtype=torch.bfloat16, device="cuda")
+    idx = torch.zeros(2, 3, 5, dtype=torch.int32, device="cuda")
+    cnt = torch.ones(2, 3, dtype=torch.int32, device="cuda")
+    for bad in (dict(Q=Q[:1]), dict(Q=Q.float()), dict(Q=Q[:, :, :3]), dict(indices=idx.long()),
+                dict(indices=idx[:, :2]), dict(counts=cnt[:1]), dict(out=Q.float()),
+                dict(Q=Q.transpose(1, 2)), dict(scale=0.0), dict(scale=float("nan"))):
+        args = dict(Q=Q, indices=idx, counts=cnt)
+        args.update(bad)
+        with pytest.raises((ValueError, TypeError, lsa.LsaError)):
+            lsa.lsa_paged_attn(c, args.pop("Q"), args.pop("indices"), args.pop("counts"), **args)
+    assert lsa.kernel_launches() == n0
+    # empty calls are allowed and launch nothing
+    lsa.lsa_paged_append(c, k[:, :0], k[:, :0], st)
+    assert lsa.lsa_paged_attn(c, Q[:, :0].contiguous(), idx[:, :0].contiguous(),
+                              cnt[:, :0].contiguous()).shape == (2, 0, 4, 64)
+    assert lsa.kernel_launches() == n0

@@ -1,0 +1,123 @@
+"""The paged cache's entries refuse bad arguments on the host, before any launch,
+and the plain binary64 forms that the GPU tests compare with agree with torch."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import long_context_indexing_b200 as lsa
+import paged_plain as plain
+
+FAKE = 1 << 22
+
+
+def _kv(**over):
+    f = dict(K=FAKE, V=FAKE, scales=FAKE, page_table=FAKE, status=FAKE, B=2, n_pages=10,
+             max_pages=5, page=64, Hkv=2, d=128, format=lsa.KV_E4M3)
+    f.update(over)
+    return lsa.PagedKV(*[f[n] for n, _ in lsa.PagedKV._fields_])
+
+
+def _append(kv=None, **over):
+    a = dict(k=FAKE, ks=256, v=FAKE, vs=256, q=FAKE, qs=1024, q_out=FAKE, Nq=3, Hq=8, start=FAKE,
+             n_new=None, inv=FAKE, rot=128, inter=0, stream=None)
+    a.update(over)
+    return lsa._lib.lsa_paged_append(None if kv == 0 else ctypes.byref(kv or _kv()), *a.values())
+
+
+def _attn(kv=None, **over):
+    a = dict(Q=FAKE, Nq=3, Hq=8, idx=FAKE, cnt=FAKE, s_max=10, scale=0.1, O=FAKE, lse=None,
+             stream=None)
+    a.update(over)
+    return lsa._lib.lsa_paged_attn(None if kv == 0 else ctypes.byref(kv or _kv()), *a.values())
+
+
+@pytest.mark.parametrize("call", [_append, _attn])
+@pytest.mark.parametrize("over,code", [
+    (dict(K=None), 1), (dict(V=None), 1), (dict(page_table=None), 1), (dict(status=None), 1),
+    (dict(scales=None), 1), (dict(format=2), 1), (dict(B=0), 1), (dict(B=65536), 1),
+    (dict(page=48), 7), (dict(page=8), 7), (dict(page=2048), 7), (dict(page=0), 7),
+    (dict(n_pages=0), 1), (dict(max_pages=0), 1), (dict(max_pages=1 << 26), 1),
+    (dict(d=96), 7), (dict(Hkv=0), 1), (dict(Hkv=3), 1), (dict(K=FAKE + 8), 2),
+    (dict(scales=FAKE + 4), 2), (dict(status=FAKE + 4), 2)])
+def test_cache_descriptions_refused(call, over, code):
+    # (Hkv = 3 with 8 query heads and rows of 256 elements fits neither call)
+    assert call(_kv(**over)) == code
+    assert lsa._lib.lsa_last_error() != b""
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(k=None), 1), (dict(v=None), 1), (dict(start=None), 1), (dict(q=None), 1),
+    (dict(q_out=None), 1), (dict(Nq=-1), 1), (dict(Nq=1 << 31), 1), (dict(Hq=0), 1),
+    (dict(Hq=7), 1), (dict(ks=255), 1), (dict(vs=248), 1), (dict(ks=260), 2), (dict(qs=1016), 1),
+    (dict(qs=1032), 1),            # q_out == q with rows apart
+    (dict(rot=130), 1), (dict(rot=8), 1), (dict(rot=144), 1), (dict(rot=-16), 1),
+    (dict(inv=None), 1), (dict(k=FAKE + 2), 2), (dict(q_out=FAKE + 8), 2), (dict(inv=FAKE + 4), 2)])
+def test_append_arguments_refused(over, code):
+    assert _append(**over) == code
+    assert lsa._lib.lsa_last_error() != b""
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(Q=None), 1), (dict(idx=None), 1), (dict(cnt=None), 1), (dict(O=None), 1),
+    (dict(Nq=-1), 1), (dict(Nq=1 << 30), 7), (dict(s_max=0), 1), (dict(Hq=7), 1),
+    (dict(scale=0.0), 1), (dict(scale=-1.0), 1), (dict(scale=float("nan")), 1),
+    (dict(scale=float("inf")), 1), (dict(Q=FAKE + 8), 2), (dict(lse=FAKE + 4), 2)])
+def test_attn_arguments_refused(over, code):
+    assert _attn(**over) == code
+    assert lsa._lib.lsa_last_error() != b""
+
+
+def test_null_cache_refused():
+    assert _append(0) == 1 and _attn(0) == 1
+    assert lsa._lib.lsa_paged_check(None, None) == 1
+
+
+def test_empty_calls_and_calls_without_gpu():
+    assert _append(Nq=0) == 0 and _attn(Nq=0) == 0
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present")
+    assert _append() == 4 and _attn() == 4            # LSA_ERR_CUDA, nothing crashes
+    assert lsa._lib.lsa_paged_check(ctypes.byref(_kv()), None) == 4
+
+
+def test_handle_wants_cuda_tensors_of_one_kind():
+    k = torch.zeros(4, 16, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        lsa.LsaPagedKV(k, k, torch.zeros(1, 4, dtype=torch.int32))
+
+
+def test_plain_grid_is_torchs_e4m3():
+    rng = np.random.default_rng(0)
+    x = np.concatenate([rng.standard_normal(20000) * np.exp2(rng.uniform(-14, 9, 20000)),
+                        np.exp2(np.arange(-14, 9)), 1.0625 * np.exp2(np.arange(-14, 8)), [0.0, 448.0]])
+    x = x.astype(np.float32).clip(-448, 448)
+    want = torch.from_numpy(x).to(torch.float8_e4m3fn).float().numpy()
+    assert np.array_equal(plain.grid(x).astype(np.float32), want)
+    assert plain.grid(np.inf) == 448 and plain.grid(-np.inf) == -448 and np.isnan(plain.grid(np.nan))
+
+
+def test_plain_scale_and_rotation():
+    assert plain.block_scale(0.0) == 2.0 ** -64 and plain.block_scale(448.0) == 1.0
+    assert plain.block_scale(np.nextafter(448.0, 500)) == 2.0 and plain.block_scale(3.5) == 2.0 ** -7
+    x = np.arange(8.0)
+    assert np.allclose(plain.rotate(x, 1, [np.pi / 2, 0.0], False), [-2, 1, 0, 3, 4, 5, 6, 7])
+    assert np.allclose(plain.rotate(x, 1, [np.pi / 2, 0.0], True), [-1, 0, 2, 3, 4, 5, 6, 7])
+
+
+def test_plain_append_and_attend_on_a_worked_case():
+    # two tokens into one block: 3.5 sets the scale 2^-7, then 7.0 doubles it; attention
+    # over one position returns its value
+    st = dict(K=np.zeros((1, 16, 1, 64)), V=np.zeros((1, 16, 1, 64)),
+              scales=np.zeros((1, 1, 2, 1)), table=np.zeros((1, 1), np.int32))
+    one = np.zeros((1, 1, 1, 64))
+    one[..., 0] = 3.5
+    plain.append(st, one, one, [0], [1], np.zeros(0), False)
+    assert st["scales"][0, 0, 0, 0] == 2.0 ** -7 and st["K"][0, 0, 0, 0] == 448
+    plain.append(st, 2 * one, one, [1], [1], np.zeros(0), False)
+    assert st["scales"][0, 0, 0, 0] == 2.0 ** -6 and st["scales"][0, 0, 1, 0] == 2.0 ** -7
+    assert st["K"][0, 0, 0, 0] == 224 and st["K"][0, 1, 0, 0] == 448
+    Kv = st["K"] * st["scales"][0, 0, 0, 0]
+    O, _, _, lse = plain.attend(Kv, Kv, st["table"], 2 * one, np.array([[[1, 0]]]), np.array([[1]]), 1.0)
+    assert O[0, 0, 0, 0] == 7.0 and lse[0, 0, 0] == 49.0
