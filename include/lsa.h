@@ -561,7 +561,8 @@ lsa_status lsa_decode_step(lsa_index* idx, void* latent_K, void* K, void* V,
  *               anything outside [0, n_pages), -1 for instance
  *   status      [8] u32, cleared by the caller before the first call
  * All of it is device memory of the caller, 16-byte aligned.  page is a power
- * of two from 16 to 1024, d is 64 or 128, max_pages * page <= 2^31 - 1.
+ * of two from 16 to 1024, d is 64 or 128; max_pages * page and n_pages * page
+ * are at most 2^31 - 1.
  * ------------------------------------------------------------------------- */
 typedef enum { LSA_KV_BF16 = 0, LSA_KV_E4M3 = 1 } lsa_kv_format;
 

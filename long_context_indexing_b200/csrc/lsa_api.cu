@@ -1273,6 +1273,8 @@ lsa_status check_paged(const lsa_paged_kv* kv)
         kv->max_pages > 2147483647LL / kv->page)
         return fail(LSA_ERR_INVALID_ARG, "bad page counts (%lld, %lld)", (long long)kv->n_pages,
                     (long long)kv->max_pages);
+    if (kv->n_pages > 2147483647LL / kv->page)
+        return fail(LSA_ERR_UNSUPPORTED, "n_pages * page > 2^31 - 1");
     if (kv->d != 64 && kv->d != 128)
         return fail(LSA_ERR_UNSUPPORTED, "d=%d not in {64,128}", kv->d);
     if (kv->Hkv < 1 || kv->Hkv > 1024)

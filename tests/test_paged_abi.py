@@ -38,7 +38,7 @@ def _attn(kv=None, **over):
     (dict(K=None), 1), (dict(V=None), 1), (dict(page_table=None), 1), (dict(status=None), 1),
     (dict(scales=None), 1), (dict(format=2), 1), (dict(B=0), 1), (dict(B=65536), 1),
     (dict(page=48), 7), (dict(page=8), 7), (dict(page=2048), 7), (dict(page=0), 7),
-    (dict(n_pages=0), 1), (dict(max_pages=0), 1), (dict(max_pages=1 << 26), 1),
+    (dict(n_pages=0), 1), (dict(max_pages=0), 1), (dict(max_pages=1 << 26), 1), (dict(n_pages=1 << 25), 7),
     (dict(d=96), 7), (dict(Hkv=0), 1), (dict(Hkv=3), 1), (dict(K=FAKE + 8), 2),
     (dict(scales=FAKE + 4), 2), (dict(status=FAKE + 4), 2)])
 def test_cache_descriptions_refused(call, over, code):
