@@ -685,8 +685,6 @@ class LsaPagedKV:
         self.device = k_pages.device
         _same_device(self.device, v_pages, page_table, scales)
         self.status = torch.zeros(8, dtype=torch.int32, device=self.device)
-        # the clearing above is ordered before calls on any stream
-        torch.cuda.current_stream(self.device).synchronize()
         self.B, self.Hkv, self.d = page_table.shape[0], Hkv, d
         self._c = PagedKV(k_pages.data_ptr(), v_pages.data_ptr(),
                           None if scales is None else scales.data_ptr(), page_table.data_ptr(),
