@@ -686,6 +686,7 @@ class LsaPagedKV:
         _same_device(self.device, v_pages, page_table, scales)
         self.status = torch.zeros(8, dtype=torch.int32, device=self.device)
         self.B, self.Hkv, self.d = page_table.shape[0], Hkv, d
+        self._index = k_pages.get_device()
         self._c = PagedKV(k_pages.data_ptr(), v_pages.data_ptr(),
                           None if scales is None else scales.data_ptr(), page_table.data_ptr(),
                           self.status.data_ptr(), self.B, n_pages, page_table.shape[1], page, Hkv,
@@ -711,27 +712,16 @@ class LsaPagedKV:
             _check(_lib.lsa_paged_check(self._ref, _stream(stream)))
 
 
-class _on:
-    """Makes `device` (and `stream`, when given) current for a call, so that launches and new
-    tensors belong to them; enters with the stream's handle."""
-
-    def __init__(self, device, stream):
-        self.device, self.stream, self.ctx = device, stream, None
-
-    def __enter__(self):
-        if self.stream is not None:
-            if self.stream.device != self.device:
-                raise ValueError("the stream is on another device")
-            self.ctx = torch.cuda.stream(self.stream)
-        elif torch.cuda.current_device() != self.device.index:
-            self.ctx = torch.cuda.device(self.device)
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return torch.cuda.current_stream(self.device).cuda_stream
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+def _elsewhere(cache, stream):
+    """None when the cache's device is current and no stream is given, else the context that
+    makes that device (and stream) current, so that launches and new tensors belong to them."""
+    if stream is None:
+        if torch._C._cuda_getDevice() == cache._index:
+            return None
+        return torch.cuda.device(cache.device)
+    if stream.device != cache.device:
+        raise ValueError("the stream is on another device")
+    return torch.cuda.stream(stream)
 
 
 def _same_device(device, *ts):
@@ -740,27 +730,37 @@ def _same_device(device, *ts):
             raise ValueError("tensors are on different devices (%s, %s)" % (t.device, device))
 
 
-def _int32(device, shape, what, t):
-    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
-        raise TypeError("%s must be a contiguous int32 tensor of shape %s" % (what, shape))
-    if t.device != device:
-        raise ValueError("%s is on another device" % what)
+def _int32(cache, t, what, shape):
+    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous() or \
+            t.get_device() != cache._index:
+        raise TypeError("%s must be a contiguous int32 tensor of shape %s on %s"
+                        % (what, shape, cache.device))
 
 
-def _token_stride(t, what, device, B, Nq, d):
-    """Elements between consecutive token rows of a bfloat16 [B][Nq][H][d] tensor whose
-    rows are contiguous (a slice of a wider projection, for instance)."""
-    if t.dtype != torch.bfloat16 or t.device != device or t.dim() != 4:
-        raise TypeError("%s must be a bfloat16 tensor [B][Nq][heads][d] on %s" % (what, device))
-    shape, st = t.shape, t.stride()
-    if shape[0] != B or shape[1] != Nq or shape[3] != d:
-        raise ValueError("%s has shape %s, not [%d][%d][heads][%d]" % (what, tuple(shape), B, Nq, d))
-    if Nq == 0:
-        return shape[2] * d
-    row = st[1] if Nq > 1 else (st[0] if B > 1 else shape[2] * d)
-    if st[3] != 1 or (shape[2] > 1 and st[2] != d) or (B > 1 and st[0] != Nq * row):
-        raise ValueError("%s must have contiguous rows at one distance (strides %s)" % (what, st))
+def _rows(cache, t, what, B, Nq, H):
+    """Elements between consecutive token rows of a bfloat16 [B][Nq][H][d] tensor whose rows
+    are contiguous (a slice of a wider projection, for instance); H None: any."""
+    if t.dtype is not torch.bfloat16 or t.dim() != 4 or t.get_device() != cache._index:
+        raise TypeError("%s must be a bfloat16 tensor [B][Nq][heads][d] on %s"
+                        % (what, cache.device))
+    b, n, h, d = t.shape
+    sb, sn, sh, se = t.stride()
+    if b != B or n != Nq or d != cache.d or (H is not None and h != H):
+        raise ValueError("%s has shape %s, not [%d][%d][%s][%d]"
+                         % (what, tuple(t.shape), B, Nq, "heads" if H is None else H, cache.d))
+    row = sn if n > 1 else (sb if b > 1 else h * d)
+    if se != 1 or (sh != d and h > 1) or (sb != n * row and b > 1 and n > 0):
+        raise ValueError("%s must have contiguous rows at one distance (strides %s)"
+                         % (what, t.stride()))
     return row
+
+
+def _like(cache, t, what, shape):
+    """A contiguous bfloat16 tensor of `shape` on the cache's device."""
+    if t.dtype is not torch.bfloat16 or t.shape != shape or not t.is_contiguous() or \
+            t.get_device() != cache._index:
+        raise TypeError("%s must be a contiguous bfloat16 tensor of shape %s on %s"
+                        % (what, tuple(shape), cache.device))
 
 
 def lsa_paged_append(cache, k, v, start, n_new=None, q=None, q_out=None, inv_freq=None,
@@ -770,39 +770,39 @@ def lsa_paged_append(cache, k, v, start, n_new=None, q=None, q_out=None, inv_fre
     rotation); tokens at and after n_new[b] are padding.  With q [B][Nq][Hq][d] the queries are
     rotated too: into q_out (which may be q; rows of padding are left as they are) or a new
     tensor, which is returned (None without q).  C: lsa_paged_append."""
-    dev = cache.device
-    B, Nq = k.shape[0], k.shape[1]
-    if B != cache.B or k.shape[2] != cache.Hkv or v.shape[2] != cache.Hkv:
-        raise ValueError("k and v must be [%d][Nq][%d][%d]" % (cache.B, cache.Hkv, cache.d))
-    ks = _token_stride(k, "k", dev, B, Nq, cache.d)
-    vs = _token_stride(v, "v", dev, B, Nq, cache.d)
-    _int32(dev, (B,), "start", start)
+    ctx = _elsewhere(cache, stream)
+    if ctx is not None:
+        with ctx:
+            return lsa_paged_append(cache, k, v, start, n_new, q, q_out, inv_freq, interleaved)
+    B, Nq = cache.B, k.shape[1]
+    ks = _rows(cache, k, "k", B, Nq, cache.Hkv)
+    vs = _rows(cache, v, "v", B, Nq, cache.Hkv)
+    _int32(cache, start, "start", (B,))
     if n_new is not None:
-        _int32(dev, (B,), "n_new", n_new)
+        _int32(cache, n_new, "n_new", (B,))
     rot = 0
     if inv_freq is not None:
-        if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1 or inv_freq.device != dev or \
-                not inv_freq.is_contiguous():
-            raise TypeError("inv_freq must be a contiguous 1-D float32 tensor on %s" % dev)
+        if inv_freq.dtype is not torch.float32 or inv_freq.dim() != 1 or \
+                not inv_freq.is_contiguous() or inv_freq.get_device() != cache._index:
+            raise TypeError("inv_freq must be a contiguous 1-D float32 tensor on %s" % cache.device)
         rot = 2 * inv_freq.shape[0]
     qs, Hq = 0, 0
-    with _on(dev, stream) as st:
-        if q is not None:
-            qs, Hq = _token_stride(q, "q", dev, B, Nq, cache.d), q.shape[2]
-            if q_out is None:
-                q_out = torch.empty(B, Nq, Hq, cache.d, dtype=torch.bfloat16, device=dev)
-            elif q_out.shape != q.shape or q_out.dtype != torch.bfloat16 or \
-                    q_out.device != dev or not q_out.is_contiguous():
-                raise ValueError("q_out must be a contiguous bfloat16 tensor of q's shape")
-        elif q_out is not None:
-            raise ValueError("q_out without q")
-        if Nq == 0:
-            return q_out
-        _check(_lib.lsa_paged_append(
-            cache._ref, k.data_ptr(), ks, v.data_ptr(), vs,
-            None if q is None else q.data_ptr(), qs, None if q is None else q_out.data_ptr(), Nq,
-            Hq, start.data_ptr(), None if n_new is None else n_new.data_ptr(),
-            None if inv_freq is None else inv_freq.data_ptr(), rot, int(interleaved), st))
+    if q is not None:
+        qs, Hq = _rows(cache, q, "q", B, Nq, None), q.shape[2]
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=cache.device)
+        else:
+            _like(cache, q_out, "q_out", q.shape)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if Nq == 0:
+        return q_out
+    _check(_lib.lsa_paged_append(
+        cache._ref, k.data_ptr(), ks, v.data_ptr(), vs, None if q is None else q.data_ptr(), qs,
+        None if q is None else q_out.data_ptr(), Nq, Hq, start.data_ptr(),
+        None if n_new is None else n_new.data_ptr(),
+        None if inv_freq is None else inv_freq.data_ptr(), rot, bool(interleaved),
+        torch._C._cuda_getCurrentRawStream(cache._index)))
     return q_out
 
 
@@ -811,26 +811,27 @@ def lsa_paged_attn(cache, Q, indices, counts, scale=None, return_lse=False, out=
     """Attention of Q [B][Nq][Hq][d] (bfloat16) over the listed positions of the paged cache
     (C: lsa_paged_attn): indices [B][Nq][s_max], counts [B][Nq] int32, as the selections return
     them.  A row of count 0 gives 0 (lse -inf)."""
-    dev = cache.device
-    if Q.dim() != 4 or Q.dtype != torch.bfloat16 or Q.device != dev or not Q.is_contiguous():
-        raise TypeError("Q must be a contiguous bfloat16 tensor [B][Nq][Hq][d] on %s" % dev)
-    B, Nq, Hq, d = Q.shape
-    if B != cache.B or d != cache.d:
+    ctx = _elsewhere(cache, stream)
+    if ctx is not None:
+        with ctx:
+            return lsa_paged_attn(cache, Q, indices, counts, scale, return_lse, out)
+    shape = Q.shape
+    _like(cache, Q, "Q", shape)
+    if len(shape) != 4 or shape[0] != cache.B or shape[3] != cache.d:
         raise ValueError("Q must be [%d][Nq][Hq][%d]" % (cache.B, cache.d))
+    B, Nq, Hq, d = shape
     s_max = indices.shape[-1]
-    _int32(dev, (B, Nq, s_max), "indices", indices)
-    _int32(dev, (B, Nq), "counts", counts)
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    if out is not None and (out.shape != Q.shape or out.dtype != torch.bfloat16 or
-                            out.device != dev or not out.is_contiguous()):
-        raise ValueError("out must be a contiguous bfloat16 tensor of Q's shape")
-    with _on(dev, stream) as st:
-        O = out if out is not None else torch.empty_like(Q)
-        lse = torch.empty(B, Nq, Hq, dtype=torch.float32, device=dev) if return_lse else None
-        if Nq == 0:
-            return (O, lse) if return_lse else O
-        _check(_lib.lsa_paged_attn(cache._ref, Q.data_ptr(), Nq, Hq, indices.data_ptr(),
-                                   counts.data_ptr(), s_max, scale, O.data_ptr(),
-                                   None if lse is None else lse.data_ptr(), st))
-    return (O, lse) if return_lse else O
+    _int32(cache, indices, "indices", (B, Nq, s_max))
+    _int32(cache, counts, "counts", (B, Nq))
+    if out is None:
+        out = torch.empty_like(Q)
+    else:
+        _like(cache, out, "out", shape)
+    lse = torch.empty((B, Nq, Hq), dtype=torch.float32, device=cache.device) if return_lse else None
+    if Nq > 0:
+        _check(_lib.lsa_paged_attn(
+            cache._ref, Q.data_ptr(), Nq, Hq, indices.data_ptr(), counts.data_ptr(), s_max,
+            1.0 / math.sqrt(d) if scale is None else scale, out.data_ptr(),
+            None if lse is None else lse.data_ptr(),
+            torch._C._cuda_getCurrentRawStream(cache._index)))
+    return (out, lse) if return_lse else out
