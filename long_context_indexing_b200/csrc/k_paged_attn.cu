@@ -150,15 +150,17 @@ __global__ void __launch_bounds__(PT_THREADS, 3) paged_attn_kernel(lsa_paged_kv 
     const int step = (int)n_cta * PT_WARPS;
     int tile = (int)rank * PT_WARPS + warp;
 
-    // position and slot of this lane's key of a tile; -1: none
+    // position of this lane's key of a tile (-2: none), its page, its slot (-1:
+    // none).  A page is looked at one tile after its look-up.
     auto position = [&](int ti) {
         const int k = ti * C::KT + lane;
-        return (lane < C::KT && k < n) ? idx[k] : -2;
+        return (lane < C::KT && k < n) ? __ldg(idx + k) : -2;
     };
-    auto slot_of = [&](int32_t t) {
+    auto page = [&](int32_t t) {
+        return (t >= 0 && t < t_end) ? __ldg(table + (t >> a.page_shift)) : -1;
+    };
+    auto slot_of = [&](int32_t t, int32_t pg) {
         if (t == -2) return -1;
-        int32_t pg = -1;
-        if (t >= 0 && t < t_end) pg = table[t >> a.page_shift];
         if (pg < 0 || pg >= kv.n_pages) {
             dev_error(kv.status, DEV_BAD_PAGE, (uint32_t)t);
             return -1;
@@ -168,7 +170,7 @@ __global__ void __launch_bounds__(PT_THREADS, 3) paged_attn_kernel(lsa_paged_kv 
 
     uint32_t kw[C::MT][2][C::KW], vw[C::MT][4][C::VW];
     float ks = 0.f, vs = 0.f;                           // this lane's key's scales
-    auto load_k = [&](int32_t slot) {
+    auto load_k = [&](int32_t slot, bool full) {
 #pragma unroll
         for (int mt = 0; mt < C::MT; ++mt)
 #pragma unroll
@@ -178,8 +180,12 @@ __global__ void __launch_bounds__(PT_THREADS, 3) paged_attn_kernel(lsa_paged_kv 
 #pragma unroll
                 for (int j = 0; j < C::KW / 4; ++j) {
                     uint32_t* w = &kw[mt][u][4 * j];
-                    w[0] = w[1] = w[2] = w[3] = 0u;
-                    if (s >= 0) ldg128(w, p + j * 64);
+                    if (full) {
+                        ldg128(w, p + j * 64);
+                    } else {
+                        w[0] = w[1] = w[2] = w[3] = 0u;
+                        if (s >= 0) ldg128(w, p + j * 64);
+                    }
                 }
             }
         if (E4M3) {
@@ -191,7 +197,7 @@ __global__ void __launch_bounds__(PT_THREADS, 3) paged_attn_kernel(lsa_paged_kv 
             }
         }
     };
-    auto load_v = [&](int32_t slot) {
+    auto load_v = [&](int32_t slot, bool full) {
 #pragma unroll
         for (int mt = 0; mt < C::MT; ++mt)
 #pragma unroll
@@ -199,30 +205,44 @@ __global__ void __launch_bounds__(PT_THREADS, 3) paged_attn_kernel(lsa_paged_kv 
                 const int32_t s =
                     __shfl_sync(0xffffffffu, slot, mt * 16 + (u >> 1) * 8 + 2 * t4 + (u & 1));
                 const char* p = Vb + s * tok_bytes;
+                uint32_t* w = vw[mt][u];
+                if (!full) {
+#pragma unroll
+                    for (int j = 0; j < C::VW; ++j) w[j] = 0u;
+                    if (s < 0) continue;
+                }
                 if (C::VW == 2) {
-                    uint32_t* w = vw[mt][u];
-                    w[0] = w[1] = 0u;
-                    if (s >= 0) ldg64(w, p);
+                    ldg64(w, p);
                 } else {
 #pragma unroll
-                    for (int j = 0; j < C::VW / 4; ++j) {
-                        uint32_t* w = &vw[mt][u][4 * j];
-                        w[0] = w[1] = w[2] = w[3] = 0u;
-                        if (s >= 0) ldg128(w, p + j * 128);
-                    }
+                    for (int j = 0; j < C::VW / 4; ++j) ldg128(w + 4 * j, p + j * 128);
                 }
             }
     };
+    // a tile without gaps loads without predicates
+    constexpr uint32_t FULL = C::KT == 32 ? 0xffffffffu : 0xffffu;
+    auto load_tile_k = [&](int32_t slot, uint32_t valid) {
+        if (valid == FULL) load_k(slot, true);
+        else load_k(slot, false);
+    };
+    auto load_tile_v = [&](int32_t slot, uint32_t valid) {
+        if (valid == FULL) load_v(slot, true);
+        else load_v(slot, false);
+    };
 
     // the first tiles' positions and slots while the queries are read
-    int32_t slot = -1, slot1 = -1, pos2 = -2;
+    int32_t slot = -1, pos1 = -2, pg1 = -1, pos2 = -2;
+    uint32_t valid = 0;
     if (tile < n_tiles) {
-        const int32_t p0 = position(tile), p1 = position(tile + step);
+        const int32_t p0 = position(tile);
+        pos1 = position(tile + step);
         pos2 = position(tile + 2 * step);
-        slot = slot_of(p0);
-        slot1 = slot_of(p1);
-        load_k(slot);
-        load_v(slot);
+        const int32_t pg0 = page(p0);
+        pg1 = page(pos1);
+        slot = slot_of(p0, pg0);
+        valid = __ballot_sync(0xffffffffu, slot >= 0);
+        load_tile_k(slot, valid);
+        load_tile_v(slot, valid);
     }
 
     // Q fragments: head r8; element order as K's lanes take their bytes
@@ -291,7 +311,6 @@ __global__ void __launch_bounds__(PT_THREADS, 3) paged_attn_kernel(lsa_paged_kv 
                                         qb[s][1]);
             }
         }
-        const uint32_t valid = __ballot_sync(0xffffffffu, slot >= 0);
         float kf[C::MT][2], ev[C::MT][2];
         if (E4M3) {
             const float lv = __log2f(fmaxf(vs, 1e-37f));
@@ -304,8 +323,10 @@ __global__ void __launch_bounds__(PT_THREADS, 3) paged_attn_kernel(lsa_paged_kv 
                 }
         }
         // the next tile's K and scales take the registers
-        slot = slot1;
-        load_k(slot);
+        const uint32_t have = valid;
+        slot = slot_of(pos1, pg1);
+        valid = __ballot_sync(0xffffffffu, slot >= 0);
+        load_tile_k(slot, valid);
 
         bool over = false;
 #pragma unroll
@@ -313,11 +334,21 @@ __global__ void __launch_bounds__(PT_THREADS, 3) paged_attn_kernel(lsa_paged_kv 
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int u = i >> 1;
-                float x = z[mt][i] * (E4M3 ? kf[mt][u] * cq[i & 1] : cq[i & 1]);
-                if (!(valid >> (mt * 16 + u * 8 + r8) & 1)) x = -INFINITY;
-                z[mt][i] = x;
-                over |= x > m1[i & 1] + PT_SLACK;
-                if (E4M3) over |= x + ev[mt][u] > m2[i & 1] + PT_SLACK;
+                z[mt][i] *= E4M3 ? kf[mt][u] * cq[i & 1] : cq[i & 1];
+            }
+        if (have != FULL) {
+#pragma unroll
+            for (int mt = 0; mt < C::MT; ++mt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (!(have >> (mt * 16 + (i >> 1) * 8 + r8) & 1)) z[mt][i] = -INFINITY;
+        }
+#pragma unroll
+        for (int mt = 0; mt < C::MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                over |= z[mt][i] > m1[i & 1] + PT_SLACK;
+                if (E4M3) over |= z[mt][i] + ev[mt][i >> 1] > m2[i & 1] + PT_SLACK;
             }
         if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
@@ -389,8 +420,9 @@ __global__ void __launch_bounds__(PT_THREADS, 3) paged_attn_kernel(lsa_paged_kv 
                     ptx::mma_bf16_16816(acc[w], a0, a1, a2, a3, pl[mt][0], pl[mt][1]);
                 }
             }
-        load_v(slot);
-        slot1 = slot_of(pos2);
+        load_tile_v(slot, valid);
+        pos1 = pos2;
+        pg1 = page(pos1);
         pos2 = position(tile + 3 * step);
     }
 
