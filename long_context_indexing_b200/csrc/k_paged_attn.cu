@@ -82,6 +82,10 @@ __device__ __forceinline__ void ldg64(uint32_t* r, const void* p)
                  : "=r"(r[0]), "=r"(r[1])
                  : "l"(p));
 }
+__device__ __forceinline__ void prefetch_l2(const void* p)
+{
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+}
 __device__ __forceinline__ float ex2(float x)
 {
     float r;
@@ -230,19 +234,36 @@ __global__ void __launch_bounds__(PT_THREADS, 3) paged_attn_kernel(lsa_paged_kv 
         else load_v(slot, false);
     };
 
-    // the first tiles' positions and slots while the queries are read
-    int32_t slot = -1, pos1 = -2, pg1 = -1, pos2 = -2;
+    // brings this lane's key's rows of a tile two ahead into L2
+    auto prefetch = [&](int32_t slot) {
+        if (slot < 0) return;
+        const int64_t off = slot * tok_bytes + (int64_t)g * C::ROWB;
+#pragma unroll
+        for (int x = 0; x < C::ROWB; x += 128) {
+            prefetch_l2((const char*)kv.K + off + x);
+            prefetch_l2((const char*)kv.V + off + x);
+        }
+    };
+
+    // the first tiles' positions and slots while the queries are read: in the
+    // loop, slot is the tile's, slot1 and slot2 the next two tiles' (slot2's rows
+    // on their way to L2), pos3 / pg3 and pos4 look two tiles further
+    int32_t slot = -1, slot1 = -1, slot2 = -1, pos3 = -2, pg3 = -1, pos4 = -2;
     uint32_t valid = 0;
     if (tile < n_tiles) {
-        const int32_t p0 = position(tile);
-        pos1 = position(tile + step);
-        pos2 = position(tile + 2 * step);
-        const int32_t pg0 = page(p0);
-        pg1 = page(pos1);
-        slot = slot_of(p0, pg0);
+        const int32_t p0 = position(tile), p1 = position(tile + step), p2 = position(tile + 2 * step);
+        pos3 = position(tile + 3 * step);
+        pos4 = position(tile + 4 * step);
+        const int32_t g0 = page(p0), g1 = page(p1), g2 = page(p2);
+        pg3 = page(pos3);
+        slot = slot_of(p0, g0);
+        slot1 = slot_of(p1, g1);
+        slot2 = slot_of(p2, g2);
         valid = __ballot_sync(0xffffffffu, slot >= 0);
         load_tile_k(slot, valid);
         load_tile_v(slot, valid);
+        prefetch(slot1);
+        prefetch(slot2);
     }
 
     // Q fragments: head r8; element order as K's lanes take their bytes
@@ -324,7 +345,7 @@ __global__ void __launch_bounds__(PT_THREADS, 3) paged_attn_kernel(lsa_paged_kv 
         }
         // the next tile's K and scales take the registers
         const uint32_t have = valid;
-        slot = slot_of(pos1, pg1);
+        slot = slot1;
         valid = __ballot_sync(0xffffffffu, slot >= 0);
         load_tile_k(slot, valid);
 
@@ -421,9 +442,12 @@ __global__ void __launch_bounds__(PT_THREADS, 3) paged_attn_kernel(lsa_paged_kv 
                 }
             }
         load_tile_v(slot, valid);
-        pos1 = pos2;
-        pg1 = page(pos1);
-        pos2 = position(tile + 3 * step);
+        slot1 = slot2;
+        slot2 = slot_of(pos3, pg3);
+        prefetch(slot2);
+        pos3 = pos4;
+        pg3 = page(pos3);
+        pos4 = position(tile + 5 * step);
     }
 
     // ---- merge: lanes, warps, CTAs ----
