@@ -6,15 +6,20 @@
 // pages, 1 for bf16).
 //
 // A unit is (query row, KV head, up to 8 of its query heads); a cluster of C
-// CTAs works on it, every warp of the cluster on tiles of KT keys of its own,
+// CTAs works on it, every warp of the cluster on tiles of 32 keys of its own,
 // and no warp waits for another until the end.  Keys are the M side of both
 // products and the query heads the N side of 8, so that a group of 8 heads
 // fills the warp MMA: S[key][head] = K Q^T, O^T[dim][head] += V^T P.
-//   * K and V go from global memory straight into the MMA's A fragments: each
-//     lane loads 16 consecutive bytes of a row and takes them as the fragment's
-//     elements, which only renames the contraction index of K (Q's fragments
-//     are renamed alike) and the output rows of V.  V's pairs along the keys
-//     are byte permutations of two rows.  No shared memory, no barrier.
+//   * A lane looks up one key of a tile: its position two tiles before the page
+//     table's entry is needed, the entry a tile before the rows are asked for,
+//     the rows brought to L2 two tiles ahead and to the warp's own ring of
+//     16-key stages in shared memory (16-byte asynchronous copies) one to two
+//     stages ahead.
+//   * A lane takes 16 consecutive bytes of a K row as fragment elements, which
+//     only renames the contraction index (Q's fragments are renamed alike), and
+//     of V rows, which renames the output rows; V's pairs along the keys are
+//     byte permutations of two rows.  Chunks are XORed with the row so that
+//     neither read meets a bank twice.
 //   * 8-bit codes become f16, which holds them exactly; a query row is scaled
 //     by a power of two so that f16 holds it too (what falls below f16's
 //     subnormals is 2^-37 of the row's largest element).  sK multiplies the
@@ -25,9 +30,10 @@
 //   * bf16 pages: the weight as the sum of two bf16 (2^-17 relative), since one
 //     would add as much error as the output's rounding.
 //   * The references m1, m2 move only when a value passes them by 2^8: one vote
-//     per tile instead of a maximum over lanes.
-// Warps, then the cluster's CTAs (through distributed shared memory) merge
-// their (m1, m2, sum, O^T).
+//     per stage instead of a maximum over lanes.
+// Warps merge their (m1, m2, sum, O^T) in shared memory; the CTAs of a cluster
+// then send each other the slice that the other finishes (distributed shared
+// memory, one barrier).
 #include "paged.cuh"
 #include "ptx.cuh"
 
@@ -36,19 +42,27 @@ namespace lsa {
 constexpr int PT_WARPS = 4;
 constexpr int PT_THREADS = 32 * PT_WARPS;
 constexpr int PT_H = 8;             // query heads of a unit
+constexpr int PT_MAX_C = 16;        // CTAs of a cluster at most
 constexpr float PT_NONE = -3e38f;   // reference before any key
 constexpr float PT_SLACK = 8.f;     // log2 that a value may pass the reference by
 
 template <bool E4M3, int D>
 struct PagedCfg {
     static constexpr int ROWB = D * (E4M3 ? 1 : 2);   // bytes of one head's row
-    // keys per tile: 64 registers of K and V in flight per lane at most
-    static constexpr int KT = ROWB > 128 ? 16 : 32;
-    static constexpr int MT = KT / 16;
     static constexpr int KW = ROWB / 16;              // words of a K row per lane
     static constexpr int VW = ROWB / 32;              // words of a V row per lane
     static constexpr int KS = D / 16;                 // contraction steps of S
     static constexpr int DT = D / 16;                 // row tiles of O^T
+    static constexpr int LPR = ROWB / 16;             // lanes (16-byte chunks) per row
+    static constexpr int RPI = 32 / LPR;              // rows per warp copy
+    static constexpr int NS = ROWB > 128 ? 2 : 3;     // stages of a warp's ring
+    static constexpr int MINB = ROWB > 128 ? 3 : 4;   // CTAs per SM
+    static constexpr int HALF = 16 * ROWB;            // bytes of a stage's K (or V)
+    static constexpr int RING = NS * 2 * HALF;        // bytes of a warp's ring
+    static constexpr int EPT = PT_H * D / PT_THREADS; // merged elements per thread
+    // the cluster's slices and the CTAs' references and sums
+    static constexpr int RECV = PT_H * D, RECV_ML = 3 * PT_H * PT_MAX_C;
+    static constexpr int BYTES = PT_WARPS * RING + 4 * (RECV + RECV_ML + 3 * PT_WARPS * PT_H);
 };
 
 struct PagedAttnArgs {
@@ -64,24 +78,6 @@ struct PagedAttnArgs {
     float* lse;
 };
 
-__device__ __forceinline__ uint32_t ldg32(const void* p)
-{
-    uint32_t r;
-    asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(r) : "l"(p));
-    return r;
-}
-__device__ __forceinline__ void ldg128(uint32_t* r, const void* p)
-{
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "l"(p));
-}
-__device__ __forceinline__ void ldg64(uint32_t* r, const void* p)
-{
-    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];"
-                 : "=r"(r[0]), "=r"(r[1])
-                 : "l"(p));
-}
 __device__ __forceinline__ void prefetch_l2(const void* p)
 {
     asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
@@ -110,28 +106,37 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
 __device__ __forceinline__ uint32_t lo_f16x2(uint32_t w) { return e4m3x2_f16x2((uint16_t)w); }
 __device__ __forceinline__ uint32_t hi_f16x2(uint32_t w) { return e4m3x2_f16x2((uint16_t)(w >> 16)); }
 
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-}
-__device__ __forceinline__ float ld_cluster(const float* p, uint32_t rank)
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank)
 {
     uint32_t a;
-    float v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(ptx::smem_addr(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-    return v;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(ptx::smem_addr(p)), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ void st_cluster(uint32_t a, float v)
+{
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+}
+__device__ __forceinline__ void st_cluster4(uint32_t a, const float* v)
+{
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(v[0]), "f"(v[1]),
+                 "f"(v[2]), "f"(v[3])
+                 : "memory");
 }
 
 template <bool E4M3, int D>
-__global__ void __launch_bounds__(PT_THREADS, 3) paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
+__global__ void __launch_bounds__(PT_THREADS, (PagedCfg<E4M3, D>::MINB))
+paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
 {
     using C = PagedCfg<E4M3, D>;
-    __shared__ float o_s[PT_WARPS][PT_H * D];
-    __shared__ float m1_s[PT_WARPS][PT_H], m2_s[PT_WARPS][PT_H], l_s[PT_WARPS][PT_H];
+    extern __shared__ __align__(128) char smem[];
+    float* recv = reinterpret_cast<float*>(smem + PT_WARPS * C::RING);
+    float* recv_ml = recv + C::RECV;                   // [CTA][m1, m2, l][head]
+    float* ml_s = recv_ml + C::RECV_ML;                // [warp][m1, m2, l][head]
     uint32_t rank, n_cta;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(n_cta));
+    // the CTAs of the cluster have started before any is written to
+    if (n_cta > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r8 = lane >> 2, t4 = lane & 3;
     const int64_t unit = blockIdx.x / n_cta;
@@ -142,155 +147,117 @@ __global__ void __launch_bounds__(PT_THREADS, 3) paged_attn_kernel(lsa_paged_kv 
     const int nh = min(PT_H, a.hpg - h0);
     const int64_t hbase = row * a.Hq + (int64_t)g * a.hpg + h0;
     const int64_t b = row / a.Nq;
-    const int n = min(max(a.counts[row], 0), a.s_max);
+    const int n = min(max(__ldg(a.counts + row), 0), a.s_max);
     const int32_t* idx = a.indices + row * a.s_max;
     const int32_t* table = kv.page_table + b * kv.max_pages;
     const int64_t t_end = kv.max_pages << a.page_shift;
     const int64_t tok_bytes = (int64_t)kv.Hkv * C::ROWB;
-    const char* Kb = (const char*)kv.K + (int64_t)g * C::ROWB + t4 * 16;
-    const char* Vb = (const char*)kv.V + (int64_t)g * C::ROWB + r8 * (E4M3 ? D / 8 : 16);
-
-    const int n_tiles = (n + C::KT - 1) / C::KT;
+    const char* Kb = (const char*)kv.K + (int64_t)g * C::ROWB;
+    const char* Vb = (const char*)kv.V + (int64_t)g * C::ROWB;
+    const int n_tiles = (n + 31) / 32;
     const int step = (int)n_cta * PT_WARPS;
     int tile = (int)rank * PT_WARPS + warp;
 
-    // position of this lane's key of a tile (-2: none), its page, its slot (-1:
-    // none).  A page is looked at one tile after its look-up.
+    // position of this lane's key of a tile, its page, its slot (-1: none).  A
+    // page is looked at one tile after its look-up.
+    // (positions are asked for before the row's count is known)
     auto position = [&](int ti) {
-        const int k = ti * C::KT + lane;
-        return (lane < C::KT && k < n) ? __ldg(idx + k) : -2;
+        const int k = ti * 32 + lane;
+        return k < a.s_max ? __ldg(idx + k) : -1;
     };
     auto page = [&](int32_t t) {
         return (t >= 0 && t < t_end) ? __ldg(table + (t >> a.page_shift)) : -1;
     };
-    auto slot_of = [&](int32_t t, int32_t pg) {
-        if (t == -2) return -1;
+    auto slot_of = [&](int32_t t, int32_t pg, int ti) {
+        if (ti * 32 + lane >= n) return -1;
         if (pg < 0 || pg >= kv.n_pages) {
             dev_error(kv.status, DEV_BAD_PAGE, (uint32_t)t);
             return -1;
         }
         return (pg << a.page_shift) + (t & (kv.page - 1));
     };
-
-    uint32_t kw[C::MT][2][C::KW], vw[C::MT][4][C::VW];
-    float ks = 0.f, vs = 0.f;                           // this lane's key's scales
-    auto load_k = [&](int32_t slot, bool full) {
-#pragma unroll
-        for (int mt = 0; mt < C::MT; ++mt)
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int32_t s = __shfl_sync(0xffffffffu, slot, mt * 16 + u * 8 + r8);
-                const char* p = Kb + s * tok_bytes;
-#pragma unroll
-                for (int j = 0; j < C::KW / 4; ++j) {
-                    uint32_t* w = &kw[mt][u][4 * j];
-                    if (full) {
-                        ldg128(w, p + j * 64);
-                    } else {
-                        w[0] = w[1] = w[2] = w[3] = 0u;
-                        if (s >= 0) ldg128(w, p + j * 64);
-                    }
-                }
-            }
-        if (E4M3) {
-            ks = vs = 0.f;
-            if (slot >= 0) {
-                const float* s = kv.scales + (int64_t)(slot / SCALE_BLOCK) * (2 * kv.Hkv) + g;
-                ks = __uint_as_float(ldg32(s));
-                vs = __uint_as_float(ldg32(s + kv.Hkv));
-            }
-        }
-    };
-    auto load_v = [&](int32_t slot, bool full) {
-#pragma unroll
-        for (int mt = 0; mt < C::MT; ++mt)
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int32_t s =
-                    __shfl_sync(0xffffffffu, slot, mt * 16 + (u >> 1) * 8 + 2 * t4 + (u & 1));
-                const char* p = Vb + s * tok_bytes;
-                uint32_t* w = vw[mt][u];
-                if (!full) {
-#pragma unroll
-                    for (int j = 0; j < C::VW; ++j) w[j] = 0u;
-                    if (s < 0) continue;
-                }
-                if (C::VW == 2) {
-                    ldg64(w, p);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < C::VW / 4; ++j) ldg128(w + 4 * j, p + j * 128);
-                }
-            }
-    };
-    // a tile without gaps loads without predicates
-    constexpr uint32_t FULL = C::KT == 32 ? 0xffffffffu : 0xffffu;
-    auto load_tile_k = [&](int32_t slot, uint32_t valid) {
-        if (valid == FULL) load_k(slot, true);
-        else load_k(slot, false);
-    };
-    auto load_tile_v = [&](int32_t slot, uint32_t valid) {
-        if (valid == FULL) load_v(slot, true);
-        else load_v(slot, false);
-    };
-
-    // brings this lane's key's rows of a tile two ahead into L2
+    // brings this lane's key's rows into L2
     auto prefetch = [&](int32_t slot) {
         if (slot < 0) return;
-        const int64_t off = slot * tok_bytes + (int64_t)g * C::ROWB;
+        const int64_t off = slot * tok_bytes;
 #pragma unroll
         for (int x = 0; x < C::ROWB; x += 128) {
-            prefetch_l2((const char*)kv.K + off + x);
-            prefetch_l2((const char*)kv.V + off + x);
+            prefetch_l2(Kb + off + x);
+            prefetch_l2(Vb + off + x);
+        }
+    };
+    float ks = 0.f, vs = 0.f, ks1 = 0.f, vs1 = 0.f;     // scales of a tile's keys, and the next's
+    auto scales_of = [&](int32_t slot, float& k, float& v) {
+        k = v = 0.f;
+        if (E4M3 && slot >= 0) {
+            const float* s = kv.scales + (int64_t)(slot / SCALE_BLOCK) * (2 * kv.Hkv) + g;
+            k = __ldg(s);
+            v = __ldg(s + kv.Hkv);
+        }
+    };
+    // 16 keys of a tile into a stage; keys without a slot become zeros
+    char* ring = smem + warp * C::RING;
+    const int crow = lane / C::LPR, cchunk = lane % C::LPR;
+    auto copy_stage = [&](int stage, int32_t slot, int half) {
+        char* dst = ring + stage * 2 * C::HALF;
+#pragma unroll
+        for (int i = 0; i < 16 / C::RPI; ++i) {
+            const int r = i * C::RPI + crow;
+            const int32_t s = __shfl_sync(0xffffffffu, slot, half * 16 + r);
+            const int64_t src = (s < 0 ? 0 : s * tok_bytes) + cchunk * 16;
+            const uint32_t bytes = s < 0 ? 0u : 16u;
+            const int at = r * C::ROWB + cchunk * 16;
+            ptx::cp_async16_zfill(dst + (at ^ (C::ROWB >= 128 ? (r & 1) << 6 : 0)), Kb + src, bytes);
+            ptx::cp_async16_zfill(dst + C::HALF + (at ^ ((r & 6) << 4)), Vb + src, bytes);
         }
     };
 
-    // the first tiles' positions and slots while the queries are read: in the
-    // loop, slot is the tile's, slot1 and slot2 the next two tiles' (slot2's rows
-    // on their way to L2), pos3 / pg3 and pos4 look two tiles further
-    int32_t slot = -1, slot1 = -1, slot2 = -1, pos3 = -2, pg3 = -1, pos4 = -2;
-    uint32_t valid = 0;
-    if (tile < n_tiles) {
+    // Q rows, element order as K's lanes take their bytes: head r8
+    uint2 qw[C::KS];
+#pragma unroll
+    for (int s = 0; s < C::KS; ++s) {
+        const int c = E4M3 ? (s / 4) * 64 + t4 * 16 + (s % 4) * 4 : (s / 2) * 32 + t4 * 8 + (s % 2) * 4;
+        qw[s] = make_uint2(0u, 0u);
+        if (r8 < nh) qw[s] = __ldg(reinterpret_cast<const uint2*>(a.Q + (hbase + r8) * D + c));
+    }
+
+    // the first tiles: in the loop, slot is the tile's, slot1 and slot2 the next
+    // two tiles' (slot2's rows on their way to L2), pos3 / pg3 and pos4 look two
+    // tiles further
+    int32_t slot = -1, slot1 = -1, slot2 = -1, pos3 = -1, pg3 = -1, pos4 = -1;
+    if (tile * 32 < a.s_max) {
         const int32_t p0 = position(tile), p1 = position(tile + step), p2 = position(tile + 2 * step);
         pos3 = position(tile + 3 * step);
         pos4 = position(tile + 4 * step);
         const int32_t g0 = page(p0), g1 = page(p1), g2 = page(p2);
         pg3 = page(pos3);
-        slot = slot_of(p0, g0);
-        slot1 = slot_of(p1, g1);
-        slot2 = slot_of(p2, g2);
-        valid = __ballot_sync(0xffffffffu, slot >= 0);
-        load_tile_k(slot, valid);
-        load_tile_v(slot, valid);
+        slot = slot_of(p0, g0, tile);
+        scales_of(slot, ks, vs);
+        copy_stage(0, slot, 0);
+        ptx::cp_async_commit();
+        if (C::NS > 2) {
+            copy_stage(1, slot, 1);
+            ptx::cp_async_commit();
+        }
+        slot1 = slot_of(p1, g1, tile + step);
+        slot2 = slot_of(p2, g2, tile + 2 * step);
         prefetch(slot1);
         prefetch(slot2);
     }
 
-    // Q fragments: head r8; element order as K's lanes take their bytes
-    uint32_t qb[C::KS][2];
+    uint32_t qb[C::KS][2];                              // Q fragments
     float cq[2];                                        // logit factor of heads 2 t4, 2 t4 + 1
     {
-        float q[C::KS][4];
-        float amax = 0.f;
-#pragma unroll
-        for (int s = 0; s < C::KS; ++s) {
-            const int c = E4M3 ? (s / 4) * 64 + t4 * 16 + (s % 4) * 4
-                               : (s / 2) * 32 + t4 * 8 + (s % 2) * 4;
-            uint2 w = make_uint2(0u, 0u);
-            if (r8 < nh) w = *reinterpret_cast<const uint2*>(a.Q + (hbase + r8) * D + c);
-            if (!E4M3) {
-                qb[s][0] = w.x;
-                qb[s][1] = w.y;
-            }
-            q[s][0] = __uint_as_float(w.x << 16);
-            q[s][1] = __uint_as_float(w.x & 0xffff0000u);
-            q[s][2] = __uint_as_float(w.y << 16);
-            q[s][3] = __uint_as_float(w.y & 0xffff0000u);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) amax = fmaxf(amax, finite_abs(q[s][i]));
-        }
         float f = a.scale_log2;
         if (E4M3) {
+            float amax = 0.f;
+#pragma unroll
+            for (int s = 0; s < C::KS; ++s) {
+                amax = fmaxf(amax, finite_abs(__uint_as_float(qw[s].x << 16)));
+                amax = fmaxf(amax, finite_abs(__uint_as_float(qw[s].x & 0xffff0000u)));
+                amax = fmaxf(amax, finite_abs(__uint_as_float(qw[s].y << 16)));
+                amax = fmaxf(amax, finite_abs(__uint_as_float(qw[s].y & 0xffff0000u)));
+            }
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
             // amax * 2^(13 - e) in [2^13, 2^14)
@@ -299,8 +266,16 @@ __global__ void __launch_bounds__(PT_THREADS, 3) paged_attn_kernel(lsa_paged_kv 
             f *= __uint_as_float((uint32_t)(e - 13 + 127) << 23);
 #pragma unroll
             for (int s = 0; s < C::KS; ++s) {
-                qb[s][0] = pack_f16(q[s][0] * up, q[s][1] * up);
-                qb[s][1] = pack_f16(q[s][2] * up, q[s][3] * up);
+                qb[s][0] = pack_f16(__uint_as_float(qw[s].x << 16) * up,
+                                    __uint_as_float(qw[s].x & 0xffff0000u) * up);
+                qb[s][1] = pack_f16(__uint_as_float(qw[s].y << 16) * up,
+                                    __uint_as_float(qw[s].y & 0xffff0000u) * up);
+            }
+        } else {
+#pragma unroll
+            for (int s = 0; s < C::KS; ++s) {
+                qb[s][0] = qw[s].x;
+                qb[s][1] = qw[s].y;
             }
         }
         cq[0] = __shfl_sync(0xffffffffu, f, 8 * t4);
@@ -313,137 +288,159 @@ __global__ void __launch_bounds__(PT_THREADS, 3) paged_attn_kernel(lsa_paged_kv 
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
     float m1[2] = {PT_NONE, PT_NONE}, m2[2] = {PT_NONE, PT_NONE}, l[2] = {0.f, 0.f};
+    // this lane's offsets inside a stage: K rows r8, r8 + 8; V rows 2 t4 ...
+    const int k_at = (r8 * C::ROWB + t4 * 16) ^ (C::ROWB >= 128 ? (r8 & 1) << 6 : 0);
+    const int v_at = C::HALF + ((2 * t4 * C::ROWB + r8 * (E4M3 ? D / 8 : 16)) ^ (t4 << 5));
+    int stage = 0;
 
     for (; tile < n_tiles; tile += step) {
-        // ---- logits: keys mt*16 + r8 (+8), heads 2 t4 (+1) ----
-        float z[C::MT][4];
+        const uint32_t valid = __ballot_sync(0xffffffffu, slot >= 0);
+        scales_of(slot1, ks1, vs1);
+        const float lv = E4M3 ? __log2f(fmaxf(vs, 1e-37f)) : 0.f;
 #pragma unroll
-        for (int mt = 0; mt < C::MT; ++mt) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) z[mt][i] = 0.f;
-#pragma unroll
-            for (int s = 0; s < C::KS; ++s) {
-                if (E4M3)
-                    mma_f16_16816(z[mt], lo_f16x2(kw[mt][0][s]), lo_f16x2(kw[mt][1][s]),
-                                  hi_f16x2(kw[mt][0][s]), hi_f16x2(kw[mt][1][s]), qb[s][0], qb[s][1]);
-                else
-                    ptx::mma_bf16_16816(z[mt], kw[mt][0][2 * s], kw[mt][1][2 * s],
-                                        kw[mt][0][2 * s + 1], kw[mt][1][2 * s + 1], qb[s][0],
-                                        qb[s][1]);
+        for (int half = 0; half < 2; ++half) {
+            if (half == 1 && tile * 32 + 16 >= n) break;
+            ptx::cp_async_wait<C::NS - 2>();
+            __syncwarp();
+            {   // the stage read last takes the one NS - 1 further on
+                const int to = stage == 0 ? C::NS - 1 : stage - 1;
+                if (C::NS == 2 && half == 0) copy_stage(to, slot, 1);
+                else copy_stage(to, slot1, C::NS == 2 ? 0 : half);
+                ptx::cp_async_commit();
             }
-        }
-        float kf[C::MT][2], ev[C::MT][2];
-        if (E4M3) {
-            const float lv = __log2f(fmaxf(vs, 1e-37f));
-#pragma unroll
-            for (int mt = 0; mt < C::MT; ++mt)
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    kf[mt][u] = __shfl_sync(0xffffffffu, ks, mt * 16 + u * 8 + r8);
-                    ev[mt][u] = __shfl_sync(0xffffffffu, lv, mt * 16 + u * 8 + r8);
-                }
-        }
-        // the next tile's K and scales take the registers
-        const uint32_t have = valid;
-        slot = slot1;
-        valid = __ballot_sync(0xffffffffu, slot >= 0);
-        load_tile_k(slot, valid);
+            const char* st = ring + stage * 2 * C::HALF;
+            stage = stage == C::NS - 1 ? 0 : stage + 1;
 
-        bool over = false;
+            // ---- logits: keys r8, r8 + 8; heads 2 t4, 2 t4 + 1 ----
+            float z[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int mt = 0; mt < C::MT; ++mt)
+            for (int j = 0; j < C::KW / 4; ++j) {
+                // chunk 4 j + t4: bit 6 of the offset is j's lowest bit, XORed
+                const char* p = st + ((k_at + (j >> 1) * 128) ^ ((j & 1) << 6));
+                const uint4 x = *reinterpret_cast<const uint4*>(p);
+                const uint4 y = *reinterpret_cast<const uint4*>(p + 8 * C::ROWB);
+                const uint32_t k0[4] = {x.x, x.y, x.z, x.w}, k1[4] = {y.x, y.y, y.z, y.w};
+                if (E4M3) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int u = i >> 1;
-                z[mt][i] *= E4M3 ? kf[mt][u] * cq[i & 1] : cq[i & 1];
-            }
-        if (have != FULL) {
+                    for (int i = 0; i < 4; ++i)
+                        mma_f16_16816(z, lo_f16x2(k0[i]), lo_f16x2(k1[i]), hi_f16x2(k0[i]),
+                                      hi_f16x2(k1[i]), qb[4 * j + i][0], qb[4 * j + i][1]);
+                } else {
 #pragma unroll
-            for (int mt = 0; mt < C::MT; ++mt)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (!(have >> (mt * 16 + (i >> 1) * 8 + r8) & 1)) z[mt][i] = -INFINITY;
-        }
-#pragma unroll
-        for (int mt = 0; mt < C::MT; ++mt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                over |= z[mt][i] > m1[i & 1] + PT_SLACK;
-                if (E4M3) over |= z[mt][i] + ev[mt][i >> 1] > m2[i & 1] + PT_SLACK;
-            }
-        if (__any_sync(0xffffffffu, over)) {
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                float x1 = m1[c], x2 = m2[c];
-#pragma unroll
-                for (int mt = 0; mt < C::MT; ++mt)
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        x1 = fmaxf(x1, z[mt][2 * u + c]);
-                        if (E4M3) x2 = fmaxf(x2, z[mt][2 * u + c] + ev[mt][u]);
-                    }
-#pragma unroll
-                for (int o = 4; o <= 16; o <<= 1) {
-                    x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, o));
-                    if (E4M3) x2 = fmaxf(x2, __shfl_xor_sync(0xffffffffu, x2, o));
-                }
-                if (!E4M3) x2 = x1;
-                const float f2 = ex2(m2[c] - x2);
-                l[c] *= ex2(m1[c] - x1);
-                m1[c] = x1;
-                m2[c] = x2;
-#pragma unroll
-                for (int j = 0; j < C::DT; ++j) {
-                    acc[j][c] *= f2;
-                    acc[j][c + 2] *= f2;
+                    for (int i = 0; i < 2; ++i)
+                        ptx::mma_bf16_16816(z, k0[2 * i], k1[2 * i], k0[2 * i + 1], k1[2 * i + 1],
+                                            qb[2 * j + i][0], qb[2 * j + i][1]);
                 }
             }
-        }
-        // ---- weights, transposed to (keys 2 t4, 2 t4 + 1; head r8) ----
-        uint32_t pb[C::MT][2], pl[C::MT][2];
-#pragma unroll
-        for (int mt = 0; mt < C::MT; ++mt)
+            float ev[2] = {0.f, 0.f};
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const float x0 = z[mt][2 * u], x1 = z[mt][2 * u + 1];
+                if (E4M3) {
+                    const float kf = __shfl_sync(0xffffffffu, ks, half * 16 + u * 8 + r8);
+                    ev[u] = __shfl_sync(0xffffffffu, lv, half * 16 + u * 8 + r8);
+                    z[2 * u] *= kf * cq[0];
+                    z[2 * u + 1] *= kf * cq[1];
+                } else {
+                    z[2 * u] *= cq[0];
+                    z[2 * u + 1] *= cq[1];
+                }
+            }
+            if (valid != 0xffffffffu) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (!(valid >> (half * 16 + (i >> 1) * 8 + r8) & 1)) z[i] = -INFINITY;
+            }
+            bool over = false;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                over |= z[i] > m1[i & 1] + PT_SLACK;
+                if (E4M3) over |= z[i] + ev[i >> 1] > m2[i & 1] + PT_SLACK;
+            }
+            if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float x1 = fmaxf(m1[c], fmaxf(z[c], z[2 + c]));
+                    float x2 = fmaxf(m2[c], fmaxf(z[c] + ev[0], z[2 + c] + ev[1]));
+#pragma unroll
+                    for (int o = 4; o <= 16; o <<= 1) {
+                        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, o));
+                        if (E4M3) x2 = fmaxf(x2, __shfl_xor_sync(0xffffffffu, x2, o));
+                    }
+                    if (!E4M3) x2 = x1;
+                    const float f2 = ex2(m2[c] - x2);
+                    l[c] *= ex2(m1[c] - x1);
+                    m1[c] = x1;
+                    m2[c] = x2;
+#pragma unroll
+                    for (int j = 0; j < C::DT; ++j) {
+                        acc[j][c] *= f2;
+                        acc[j][c + 2] *= f2;
+                    }
+                }
+            }
+            // ---- weights, transposed to (keys 2 t4, 2 t4 + 1; head r8) ----
+            uint32_t pb[2], pl[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const float x0 = z[2 * u], x1 = z[2 * u + 1];
                 const float p0 = ex2(x0 - m1[0]), p1 = ex2(x1 - m1[1]);
                 l[0] += p0;
                 l[1] += p1;
                 if (E4M3) {
-                    const float w0 = ex2(x0 + ev[mt][u] - m2[0]), w1 = ex2(x1 + ev[mt][u] - m2[1]);
-                    pb[mt][u] = ptx::movmatrix_t(pack_f16(w0, w1));
+                    pb[u] = ptx::movmatrix_t(pack_f16(ex2(x0 + ev[u] - m2[0]), ex2(x1 + ev[u] - m2[1])));
                 } else {
                     const uint32_t hi = ptx::pack_bf16(p0, p1);
-                    const float e0 = p0 - __uint_as_float(hi << 16);
-                    const float e1 = p1 - __uint_as_float(hi & 0xffff0000u);
-                    pb[mt][u] = ptx::movmatrix_t(hi);
-                    pl[mt][u] = ptx::movmatrix_t(ptx::pack_bf16(e0, e1));
+                    pb[u] = ptx::movmatrix_t(hi);
+                    pl[u] = ptx::movmatrix_t(ptx::pack_bf16(p0 - __uint_as_float(hi << 16),
+                                                            p1 - __uint_as_float(hi & 0xffff0000u)));
                 }
             }
-        // ---- O^T += V^T P ----
+            // ---- O^T += V^T P: keys 2 t4, 2 t4 + 1, 2 t4 + 8, 2 t4 + 9 ----
+            uint32_t vw[4][C::VW];
 #pragma unroll
-        for (int mt = 0; mt < C::MT; ++mt)
+            for (int u = 0; u < 4; ++u) {
+                // row 2 t4 + (u & 1) + 8 (u >> 1): the XOR is the lane's
+                const char* p = C::ROWB >= 128
+                                    ? st + v_at + ((u & 1) + 8 * (u >> 1)) * C::ROWB
+                                    : st + ((v_at + 8 * (u >> 1) * C::ROWB) ^ ((u & 1) * C::ROWB));
+                if (C::VW == 2) {
+                    const uint2 x = *reinterpret_cast<const uint2*>(p);
+                    vw[u][0] = x.x;
+                    vw[u][1] = x.y;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < C::VW / 4; ++j) {
+                        const uint4 x = *reinterpret_cast<const uint4*>(p + j * 128);
+                        vw[u][4 * j] = x.x;
+                        vw[u][4 * j + 1] = x.y;
+                        vw[u][4 * j + 2] = x.z;
+                        vw[u][4 * j + 3] = x.w;
+                    }
+                }
+            }
 #pragma unroll
             for (int w = 0; w < C::VW; ++w) {
-                const uint32_t r0 = vw[mt][0][w], r1 = vw[mt][1][w];
-                const uint32_t r2 = vw[mt][2][w], r3 = vw[mt][3][w];
+                const uint32_t r0 = vw[0][w], r1 = vw[1][w], r2 = vw[2][w], r3 = vw[3][w];
                 if (E4M3) {
                     const uint32_t x = __byte_perm(r0, r1, 0x5140), y = __byte_perm(r2, r3, 0x5140);
                     mma_f16_16816(acc[2 * w], lo_f16x2(x), hi_f16x2(x), lo_f16x2(y), hi_f16x2(y),
-                                  pb[mt][0], pb[mt][1]);
+                                  pb[0], pb[1]);
                     const uint32_t x2 = __byte_perm(r0, r1, 0x7362), y2 = __byte_perm(r2, r3, 0x7362);
                     mma_f16_16816(acc[2 * w + 1], lo_f16x2(x2), hi_f16x2(x2), lo_f16x2(y2),
-                                  hi_f16x2(y2), pb[mt][0], pb[mt][1]);
+                                  hi_f16x2(y2), pb[0], pb[1]);
                 } else {
                     const uint32_t a0 = __byte_perm(r0, r1, 0x5410), a1 = __byte_perm(r0, r1, 0x7632);
                     const uint32_t a2 = __byte_perm(r2, r3, 0x5410), a3 = __byte_perm(r2, r3, 0x7632);
-                    ptx::mma_bf16_16816(acc[w], a0, a1, a2, a3, pb[mt][0], pb[mt][1]);
-                    ptx::mma_bf16_16816(acc[w], a0, a1, a2, a3, pl[mt][0], pl[mt][1]);
+                    ptx::mma_bf16_16816(acc[w], a0, a1, a2, a3, pb[0], pb[1]);
+                    ptx::mma_bf16_16816(acc[w], a0, a1, a2, a3, pl[0], pl[1]);
                 }
             }
-        load_tile_v(slot, valid);
+        }
+        slot = slot1;
+        ks = ks1;
+        vs = vs1;
         slot1 = slot2;
-        slot2 = slot_of(pos3, pg3);
+        slot2 = slot_of(pos3, pg3, tile + 3 * step);
         prefetch(slot2);
         pos3 = pos4;
         pg3 = page(pos3);
@@ -451,80 +448,108 @@ __global__ void __launch_bounds__(PT_THREADS, 3) paged_attn_kernel(lsa_paged_kv 
     }
 
     // ---- merge: lanes, warps, CTAs ----
+    ptx::cp_async_wait<0>();
+    __syncwarp();                                       // the ring is free
+    float* o_s = reinterpret_cast<float*>(smem);        // warp w's O^T at w * RING
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
 #pragma unroll
         for (int o = 4; o <= 16; o <<= 1) l[c] += __shfl_xor_sync(0xffffffffu, l[c], o);
         if (r8 == 0) {
-            m1_s[warp][2 * t4 + c] = m1[c];
-            m2_s[warp][2 * t4 + c] = E4M3 ? m2[c] : m1[c];
-            l_s[warp][2 * t4 + c] = l[c];
+            float* ml = ml_s + warp * 3 * PT_H + 2 * t4 + c;
+            ml[0] = m1[c];
+            ml[PT_H] = E4M3 ? m2[c] : m1[c];
+            ml[2 * PT_H] = l[c];
         }
     }
-#pragma unroll
-    for (int j = 0; j < C::DT; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            // row tile j: dims of V's word j / 2 (8-bit) or j (bf16) of the lane
-            const int dim = E4M3 ? r8 * (D / 8) + 2 * j + (i >> 1)
-                                 : (j / 4) * 64 + r8 * 8 + 2 * (j % 4) + (i >> 1);
-            o_s[warp][(2 * t4 + (i & 1)) * D + dim] = acc[j][i];
-        }
-    __syncthreads();
-    // the CTA's warps into warp 0's arrays
-    constexpr int EPT = PT_H * D / PT_THREADS;          // elements per thread, one head's
+    // [row tile and half][head parity][head pair][r8]: no bank met twice
     {
-        const int h = threadIdx.x * EPT / D;
-        float M2 = m2_s[0][h];
+        float* mine = reinterpret_cast<float*>(ring);
 #pragma unroll
-        for (int w = 1; w < PT_WARPS; ++w) M2 = fmaxf(M2, m2_s[w][h]);
-        float o[EPT];
+        for (int j = 0; j < C::DT; ++j)
 #pragma unroll
-        for (int i = 0; i < EPT; ++i) o[i] = 0.f;
-#pragma unroll
-        for (int w = 0; w < PT_WARPS; ++w) {
-            const float f = ex2(m2_s[w][h] - M2);
-#pragma unroll
-            for (int i = 0; i < EPT; ++i) o[i] += f * o_s[w][threadIdx.x * EPT + i];
-        }
-        float M1 = PT_NONE, L = 0.f;
-        if (threadIdx.x < PT_H) {
-#pragma unroll
-            for (int w = 0; w < PT_WARPS; ++w) M1 = fmaxf(M1, m1_s[w][threadIdx.x]);
-#pragma unroll
-            for (int w = 0; w < PT_WARPS; ++w)
-                L += l_s[w][threadIdx.x] * ex2(m1_s[w][threadIdx.x] - M1);
-        }
-        __syncthreads();
-        if (threadIdx.x < PT_H) {
-            m1_s[0][threadIdx.x] = M1;
-            l_s[0][threadIdx.x] = L;
-        }
-        if ((threadIdx.x * EPT) % D == 0) m2_s[0][h] = M2;
-#pragma unroll
-        for (int i = 0; i < EPT; ++i) o_s[0][threadIdx.x * EPT + i] = o[i];
+            for (int i = 0; i < 4; ++i)
+                mine[(2 * j + (i >> 1)) * 64 + (i & 1) * 32 + t4 * 8 + r8] = acc[j][i];
     }
-    if (n_cta > 1) cluster_sync();
-    else __syncthreads();
-    // the cluster's CTAs share the output's elements
-    const int total = nh * D;
-    for (int x = (int)rank * PT_THREADS + threadIdx.x; x < total; x += (int)n_cta * PT_THREADS) {
-        const int h = x / D;
-        float M1 = PT_NONE, M2 = PT_NONE, L = 0.f, o = 0.f;
-        for (uint32_t c = 0; c < n_cta; ++c) {
-            M1 = fmaxf(M1, ld_cluster(&m1_s[0][h], c));
-            M2 = fmaxf(M2, ld_cluster(&m2_s[0][h], c));
-        }
-        for (uint32_t c = 0; c < n_cta; ++c) {
-            L += ld_cluster(&l_s[0][h], c) * ex2(ld_cluster(&m1_s[0][h], c) - M1);
-            o += ld_cluster(&o_s[0][x], c) * ex2(ld_cluster(&m2_s[0][h], c) - M2);
-        }
-        o = L == 0.f ? 0.f : o / L * ex2(M2 - M1);
-        a.O[hbase * D + x] = __float2bfloat16_rn(o);
-        if (a.lse && x % D == 0)
-            a.lse[hbase + h] = L == 0.f ? -INFINITY : (M1 + log2f(L)) * 0.6931471805599453f;
+    __syncthreads();
+    // a thread: one (head, r8) and EPT consecutive dims
+    const int combo = threadIdx.x & 63, part = threadIdx.x >> 6;
+    const int h = 2 * (combo >> 3 & 3) + (combo >> 5);
+    const int dr = combo & 7;
+    const int dim = E4M3 ? dr * (D / 8) + part * C::EPT
+                         : (C::EPT == 8 ? part * 64 + dr * 8 : dr * 8 + part * 4);
+    float M1 = PT_NONE, M2 = PT_NONE, L = 0.f, o[C::EPT];
+#pragma unroll
+    for (int w = 0; w < PT_WARPS; ++w) {
+        M1 = fmaxf(M1, ml_s[w * 3 * PT_H + h]);
+        M2 = fmaxf(M2, ml_s[w * 3 * PT_H + PT_H + h]);
     }
-    if (n_cta > 1) cluster_sync();       // no CTA leaves while another reads its arrays
+#pragma unroll
+    for (int i = 0; i < C::EPT; ++i) o[i] = 0.f;
+#pragma unroll
+    for (int w = 0; w < PT_WARPS; ++w) {
+        const float* ml = ml_s + w * 3 * PT_H + h;
+        const float f = ex2(ml[PT_H] - M2);
+        L += ml[2 * PT_H] * ex2(ml[0] - M1);
+        const float* src = o_s + w * (C::RING / 4) + part * C::EPT * 64 + combo;
+#pragma unroll
+        for (int i = 0; i < C::EPT; ++i) o[i] += f * src[i * 64];
+    }
+    if (n_cta > 1) {
+        asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+        // thread t's elements go to CTA t / tpc, place (source CTA, t % tpc)
+        const uint32_t tpc = PT_THREADS / n_cta;
+        const uint32_t to = threadIdx.x / tpc, at = threadIdx.x % tpc;
+        const uint32_t dst = cluster_addr(recv, to) + 4 * C::EPT * (rank * tpc + at);
+#pragma unroll
+        for (int i = 0; i < C::EPT; i += 4) st_cluster4(dst + 4 * i, o + i);
+        const uint32_t ml = cluster_addr(recv_ml, to) + 4 * (rank * 3 * PT_H + h);
+        st_cluster(ml, M1);                             // (equal values from a head's threads)
+        st_cluster(ml + 4 * PT_H, M2);
+        st_cluster(ml + 8 * PT_H, L);
+        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
+                     ::: "memory");
+    }
+    if (n_cta == 1) {
+        const float f = L == 0.f ? 0.f : ex2(M2 - M1) / L;
+        if (h < nh) {
+            __nv_bfloat16* dst = a.O + (hbase + h) * D + dim;
+            uint32_t w[C::EPT / 2];
+#pragma unroll
+            for (int i = 0; i < C::EPT / 2; ++i)
+                w[i] = ptx::pack_bf16(L == 0.f ? 0.f : o[2 * i] * f, L == 0.f ? 0.f : o[2 * i + 1] * f);
+            if (C::EPT == 8) *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+            else *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+            if (a.lse && dim == 0)
+                a.lse[hbase + h] = L == 0.f ? -INFINITY : (M1 + log2f(L)) * 0.6931471805599453f;
+        }
+        return;
+    }
+    // this CTA finishes the elements of threads rank * tpc .. of every CTA
+    const uint32_t tpc = PT_THREADS / n_cta;
+    for (uint32_t x = threadIdx.x; x < tpc * C::EPT; x += PT_THREADS) {
+        const uint32_t t = rank * tpc + x / C::EPT, i = x % C::EPT;
+        const int cb = t & 63, pt = t >> 6, hh = 2 * (cb >> 3 & 3) + (cb >> 5), rr = cb & 7;
+        const int dd = (E4M3 ? rr * (D / 8) + pt * C::EPT
+                             : (C::EPT == 8 ? pt * 64 + rr * 8 : rr * 8 + pt * 4)) + i;
+        float N1 = PT_NONE, N2 = PT_NONE, S = 0.f, v = 0.f;
+#pragma unroll 4
+        for (uint32_t c = 0; c < n_cta; ++c) {
+            N1 = fmaxf(N1, recv_ml[c * 3 * PT_H + hh]);
+            N2 = fmaxf(N2, recv_ml[c * 3 * PT_H + PT_H + hh]);
+        }
+#pragma unroll 4
+        for (uint32_t c = 0; c < n_cta; ++c) {
+            const float* ml = recv_ml + c * 3 * PT_H + hh;
+            S += ml[2 * PT_H] * ex2(ml[0] - N1);
+            v += recv[c * tpc * C::EPT + x] * ex2(ml[PT_H] - N2);
+        }
+        if (hh < nh) {
+            a.O[(hbase + hh) * D + dd] = __float2bfloat16_rn(S == 0.f ? 0.f : v * (ex2(N2 - N1) / S));
+            if (a.lse && dd == 0)
+                a.lse[hbase + hh] = S == 0.f ? -INFINITY : (N1 + log2f(S)) * 0.6931471805599453f;
+        }
+    }
 }
 
 cudaError_t launch_paged_attn(const lsa_paged_kv& kv, const void* Q, int64_t Nq, int Hq,
@@ -546,14 +571,18 @@ cudaError_t launch_paged_attn(const lsa_paged_kv& kv, const void* Q, int64_t Nq,
     a.O = (__nv_bfloat16*)O;
     a.lse = lse;
     const int64_t units = kv.B * Nq * kv.Hkv * a.chunks;
-    // CTAs per unit: enough to fill the SMs three times over, each with at
-    // least a tile per warp
+    // CTAs per unit: enough to fill the SMs, each with at least a tile per warp
     int c = 1;
-    while (c < 8 && units * c * 2 <= 3 * 148 && s_max >= 2 * c * PT_WARPS * 32) c *= 2;
-    auto run = [&](auto kern) {
+    while (c < PT_MAX_C && units * c * 2 <= 4 * 148 && s_max >= 2 * c * PT_WARPS * 32) c *= 2;
+    auto run = [&](auto kern, int bytes) {
+        cudaError_t e = ensure_smem_attr((const void*)kern, bytes);
+        if (e == cudaSuccess && c > 8)
+            e = cudaFuncSetAttribute((const void*)kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(units * c));
         cfg.blockDim = dim3(PT_THREADS);
+        cfg.dynamicSmemBytes = bytes;
         cfg.stream = st;
         cudaLaunchAttribute at;
         at.id = cudaLaunchAttributeClusterDimension;
@@ -565,9 +594,11 @@ cudaError_t launch_paged_attn(const lsa_paged_kv& kv, const void* Q, int64_t Nq,
     };
     cudaError_t e;
     if (kv.format == LSA_KV_E4M3)
-        e = kv.d == 64 ? run(paged_attn_kernel<true, 64>) : run(paged_attn_kernel<true, 128>);
+        e = kv.d == 64 ? run(paged_attn_kernel<true, 64>, PagedCfg<true, 64>::BYTES)
+                       : run(paged_attn_kernel<true, 128>, PagedCfg<true, 128>::BYTES);
     else
-        e = kv.d == 64 ? run(paged_attn_kernel<false, 64>) : run(paged_attn_kernel<false, 128>);
+        e = kv.d == 64 ? run(paged_attn_kernel<false, 64>, PagedCfg<false, 64>::BYTES)
+                       : run(paged_attn_kernel<false, 128>, PagedCfg<false, 128>::BYTES);
     if (e != cudaSuccess) return e;
     note_launch();
     return cudaGetLastError();
