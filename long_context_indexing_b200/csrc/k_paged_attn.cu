@@ -20,20 +20,26 @@
 //     of V rows, which renames the output rows; V's pairs along the keys are
 //     byte permutations of two rows.  Chunks are XORed with the row so that
 //     neither read meets a bank twice.
-//   * 8-bit codes become f16, which holds them exactly; a query row is scaled
-//     by a power of two so that f16 holds it too (what falls below f16's
-//     subnormals is 2^-37 of the row's largest element).  sK multiplies the
-//     logit in fp32; sV joins the exponent of the weight, w_t = 2^(z_t + log2
-//     sV_t - m2), so that the f16 weight of the largest contribution is near 1
-//     whatever the scales: 2^-11 relative.  The denominator sums 2^(z_t - m1)
-//     in fp32 with a reference of its own.
+//   * 8-bit codes become f16, which holds them exactly (the warp MMA's 8-bit
+//     form is slower here: 1,024 queries of a 1M context 455 us against 380); a
+//     unit's query rows are scaled by a power of two so that f16 holds them too
+//     (what falls below f16's subnormals is 2^-37 of their largest element).  sK
+//     multiplies the logit in fp32; sV joins the exponent of the weight, w_t =
+//     2^(z_t + log2 sV_t - m2), so that the f16 weight of the largest
+//     contribution is near 1 whatever the scales: 2^-11 relative.  The
+//     denominator sums 2^(z_t - m1) in fp32 with a reference of its own.
 //   * bf16 pages: the weight as the sum of two bf16 (2^-17 relative), since one
 //     would add as much error as the output's rounding.
 //   * The references m1, m2 move only when a value passes them by 2^8: one vote
 //     per stage instead of a maximum over lanes.
+//   * The logits of a stage are computed beside the products of the stage before
+//     (a stage of the ring holds V of 16 keys and K of the next 16), so that two
+//     independent chains of MMAs share the warp.
 // Warps merge their (m1, m2, sum, O^T) in shared memory; the CTAs of a cluster
 // then send each other the slice that the other finishes (distributed shared
 // memory, one barrier).
+#include <type_traits>
+
 #include "paged.cuh"
 #include "ptx.cuh"
 
@@ -55,6 +61,7 @@ struct PagedCfg {
     static constexpr int DT = D / 16;                 // row tiles of O^T
     static constexpr int LPR = ROWB / 16;             // lanes (16-byte chunks) per row
     static constexpr int RPI = 32 / LPR;              // rows per warp copy
+    static constexpr int RI = 16 / RPI;               // copies of 16 rows
     static constexpr int NS = ROWB > 128 ? 2 : 3;     // stages of a warp's ring
     static constexpr int MINB = ROWB > 128 ? 3 : 4;   // CTAs per SM
     static constexpr int HALF = 16 * ROWB;            // bytes of a stage's K (or V)
@@ -88,14 +95,37 @@ __device__ __forceinline__ float ex2(float x)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-__device__ __forceinline__ void mma_f16_16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2,
-                                              uint32_t a3, uint32_t b0, uint32_t b1)
+// (not volatile: the compiler orders independent products)
+__device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1)
 {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
         "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16(float* c, uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+        "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// 16 bytes to shared memory; zeros for a negative slot (its source is not read).
+template <bool FULL>
+__device__ __forceinline__ void copy16(uint32_t dst, const char* base, int32_t slot, uint32_t tok_bytes)
+{
+    if (FULL)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst),
+                     "l"(base + (uint64_t)(uint32_t)slot * tok_bytes)
+                     : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.lt.s32 p, %2, 0;\n\t"
+            "cp.async.cg.shared.global [%0], [%1], 16, p;\n\t}" ::"r"(dst),
+            "l"(base + (uint64_t)(uint32_t)max(slot, 0) * tok_bytes), "r"(slot)
+            : "memory");
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
 {
@@ -150,8 +180,8 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
     const int n = min(max(__ldg(a.counts + row), 0), a.s_max);
     const int32_t* idx = a.indices + row * a.s_max;
     const int32_t* table = kv.page_table + b * kv.max_pages;
-    const int64_t t_end = kv.max_pages << a.page_shift;
-    const int64_t tok_bytes = (int64_t)kv.Hkv * C::ROWB;
+    const int32_t t_end = (int32_t)(kv.max_pages << a.page_shift);
+    const uint32_t tok_bytes = (uint32_t)kv.Hkv * C::ROWB;
     const char* Kb = (const char*)kv.K + (int64_t)g * C::ROWB;
     const char* Vb = (const char*)kv.V + (int64_t)g * C::ROWB;
     const int n_tiles = (n + 31) / 32;
@@ -166,11 +196,11 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
         return k < a.s_max ? __ldg(idx + k) : -1;
     };
     auto page = [&](int32_t t) {
-        return (t >= 0 && t < t_end) ? __ldg(table + (t >> a.page_shift)) : -1;
+        return (uint32_t)t < (uint32_t)t_end ? __ldg(table + (t >> a.page_shift)) : -1;
     };
     auto slot_of = [&](int32_t t, int32_t pg, int ti) {
         if (ti * 32 + lane >= n) return -1;
-        if (pg < 0 || pg >= kv.n_pages) {
+        if ((uint32_t)pg >= (uint32_t)kv.n_pages) {
             dev_error(kv.status, DEV_BAD_PAGE, (uint32_t)t);
             return -1;
         }
@@ -179,7 +209,7 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
     // brings this lane's key's rows into L2
     auto prefetch = [&](int32_t slot) {
         if (slot < 0) return;
-        const int64_t off = slot * tok_bytes;
+        const uint64_t off = (uint64_t)(uint32_t)slot * tok_bytes;
 #pragma unroll
         for (int x = 0; x < C::ROWB; x += 128) {
             prefetch_l2(Kb + off + x);
@@ -195,22 +225,34 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
             v = __ldg(s + kv.Hkv);
         }
     };
-    // 16 keys of a tile into a stage; keys without a slot become zeros
+    // A stage of the ring: V of 16 keys, K of the 16 after them; keys without a
+    // slot become zeros.  The slots of the rows whose K was copied last serve V's
+    // copy of the next stage.
     char* ring = smem + warp * C::RING;
     const int crow = lane / C::LPR, cchunk = lane % C::LPR;
-    auto copy_stage = [&](int stage, int32_t slot, int half) {
-        char* dst = ring + stage * 2 * C::HALF;
+    const uint32_t c_at = crow * C::ROWB + cchunk * 16;
+    const uint32_t kc_at = ptx::smem_addr(ring) + (c_at ^ (C::ROWB >= 128 ? (crow & 1) << 6 : 0));
+    const uint32_t vc_at = ptx::smem_addr(ring) + C::HALF + (c_at ^ ((crow & 6) << 4));
+    const char* Kc = Kb + cchunk * 16;
+    const char* Vc = Vb + cchunk * 16;
+    int32_t rs[C::RI];
+    auto copy_v = [&](int stage, auto full) {
 #pragma unroll
-        for (int i = 0; i < 16 / C::RPI; ++i) {
-            const int r = i * C::RPI + crow;
-            const int32_t s = __shfl_sync(0xffffffffu, slot, half * 16 + r);
-            const int64_t src = (s < 0 ? 0 : s * tok_bytes) + cchunk * 16;
-            const uint32_t bytes = s < 0 ? 0u : 16u;
-            const int at = r * C::ROWB + cchunk * 16;
-            ptx::cp_async16_zfill(dst + (at ^ (C::ROWB >= 128 ? (r & 1) << 6 : 0)), Kb + src, bytes);
-            ptx::cp_async16_zfill(dst + C::HALF + (at ^ ((r & 6) << 4)), Vb + src, bytes);
+        for (int i = 0; i < C::RI; ++i)
+            copy16<decltype(full)::value>((vc_at ^ ((i * C::RPI & 6) << 4)) + stage * 2 * C::HALF +
+                                              i * C::RPI * C::ROWB,
+                                          Vc, rs[i], tok_bytes);
+    };
+    auto copy_k = [&](int stage, int32_t slot, int half, auto full) {
+#pragma unroll
+        for (int i = 0; i < C::RI; ++i) {
+            rs[i] = __shfl_sync(0xffffffffu, slot, half * 16 + i * C::RPI + crow);
+            copy16<decltype(full)::value>(kc_at + stage * 2 * C::HALF + i * C::RPI * C::ROWB, Kc, rs[i],
+                                          tok_bytes);
         }
     };
+    const std::false_type some{};                      // rows that may have no slot
+    const std::true_type full{};
 
     // Q rows, element order as K's lanes take their bytes: head r8
     uint2 qw[C::KS];
@@ -233,53 +275,52 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
         pg3 = page(pos3);
         slot = slot_of(p0, g0, tile);
         scales_of(slot, ks, vs);
-        copy_stage(0, slot, 0);
+        copy_k(C::NS - 1, slot, 0, some);
         ptx::cp_async_commit();
-        if (C::NS > 2) {
-            copy_stage(1, slot, 1);
-            ptx::cp_async_commit();
-        }
+        copy_v(0, some);
+        copy_k(0, slot, 1, some);
+        ptx::cp_async_commit();
         slot1 = slot_of(p1, g1, tile + step);
         slot2 = slot_of(p2, g2, tile + 2 * step);
         prefetch(slot1);
         prefetch(slot2);
+        if (C::NS > 2) {
+            copy_v(1, some);
+            copy_k(1, slot1, 0, some);
+            ptx::cp_async_commit();
+        }
     }
 
     uint32_t qb[C::KS][2];                              // Q fragments
-    float cq[2];                                        // logit factor of heads 2 t4, 2 t4 + 1
-    {
-        float f = a.scale_log2;
-        if (E4M3) {
-            float amax = 0.f;
+    float factor = a.scale_log2;                        // logit in log2 units of a product
+    if (E4M3) {
+        float amax = 0.f;                               // of the unit's rows
 #pragma unroll
-            for (int s = 0; s < C::KS; ++s) {
-                amax = fmaxf(amax, finite_abs(__uint_as_float(qw[s].x << 16)));
-                amax = fmaxf(amax, finite_abs(__uint_as_float(qw[s].x & 0xffff0000u)));
-                amax = fmaxf(amax, finite_abs(__uint_as_float(qw[s].y << 16)));
-                amax = fmaxf(amax, finite_abs(__uint_as_float(qw[s].y & 0xffff0000u)));
-            }
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-            // amax * 2^(13 - e) in [2^13, 2^14)
-            const int e = max((int)(__float_as_uint(amax) >> 23) - 127, -100);
-            const float up = __uint_as_float((uint32_t)(13 - e + 127) << 23);
-            f *= __uint_as_float((uint32_t)(e - 13 + 127) << 23);
-#pragma unroll
-            for (int s = 0; s < C::KS; ++s) {
-                qb[s][0] = pack_f16(__uint_as_float(qw[s].x << 16) * up,
-                                    __uint_as_float(qw[s].x & 0xffff0000u) * up);
-                qb[s][1] = pack_f16(__uint_as_float(qw[s].y << 16) * up,
-                                    __uint_as_float(qw[s].y & 0xffff0000u) * up);
-            }
-        } else {
-#pragma unroll
-            for (int s = 0; s < C::KS; ++s) {
-                qb[s][0] = qw[s].x;
-                qb[s][1] = qw[s].y;
-            }
+        for (int s = 0; s < C::KS; ++s) {
+            amax = fmaxf(amax, finite_abs(__uint_as_float(qw[s].x << 16)));
+            amax = fmaxf(amax, finite_abs(__uint_as_float(qw[s].x & 0xffff0000u)));
+            amax = fmaxf(amax, finite_abs(__uint_as_float(qw[s].y << 16)));
+            amax = fmaxf(amax, finite_abs(__uint_as_float(qw[s].y & 0xffff0000u)));
         }
-        cq[0] = __shfl_sync(0xffffffffu, f, 8 * t4);
-        cq[1] = __shfl_sync(0xffffffffu, f, 8 * t4 + 4);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        // amax * 2^(13 - e) in [2^13, 2^14)
+        const int e = max((int)(__float_as_uint(amax) >> 23) - 127, -100);
+        const float up = __uint_as_float((uint32_t)(13 - e + 127) << 23);
+        factor *= __uint_as_float((uint32_t)(e - 13 + 127) << 23);
+#pragma unroll
+        for (int s = 0; s < C::KS; ++s) {
+            qb[s][0] = pack_f16(__uint_as_float(qw[s].x << 16) * up,
+                                __uint_as_float(qw[s].x & 0xffff0000u) * up);
+            qb[s][1] = pack_f16(__uint_as_float(qw[s].y << 16) * up,
+                                __uint_as_float(qw[s].y & 0xffff0000u) * up);
+        }
+    } else {
+#pragma unroll
+        for (int s = 0; s < C::KS; ++s) {
+            qb[s][0] = qw[s].x;
+            qb[s][1] = qw[s].y;
+        }
     }
 
     float acc[C::DT][4];
@@ -291,90 +332,116 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
     // this lane's offsets inside a stage: K rows r8, r8 + 8; V rows 2 t4 ...
     const int k_at = (r8 * C::ROWB + t4 * 16) ^ (C::ROWB >= 128 ? (r8 & 1) << 6 : 0);
     const int v_at = C::HALF + ((2 * t4 * C::ROWB + r8 * (E4M3 ? D / 8 : 16)) ^ (t4 << 5));
+    float z[4];                                         // products of keys r8, r8 + 8 with
+                                                        // heads 2 t4, 2 t4 + 1
+    auto products = [&](const char* st) {
+        float y[4] = {0.f, 0.f, 0.f, 0.f};             // a second chain
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[i] = 0.f;
+#pragma unroll
+        for (int j = 0; j < C::KW / 4; ++j) {
+            // chunk 4 j + t4: bit 6 of the offset is j's lowest bit, XORed
+            const char* p = st + ((k_at + (j >> 1) * 128) ^ ((j & 1) << 6));
+            const uint4 u = *reinterpret_cast<const uint4*>(p);
+            const uint4 v = *reinterpret_cast<const uint4*>(p + 8 * C::ROWB);
+            const uint32_t k0[4] = {u.x, u.y, u.z, u.w}, k1[4] = {v.x, v.y, v.z, v.w};
+            if (E4M3) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    mma_f16(i & 1 ? y : z, lo_f16x2(k0[i]), lo_f16x2(k1[i]), hi_f16x2(k0[i]),
+                            hi_f16x2(k1[i]), qb[4 * j + i][0], qb[4 * j + i][1]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    mma_bf16(i ? y : z, k0[2 * i], k1[2 * i], k0[2 * i + 1], k1[2 * i + 1],
+                             qb[2 * j + i][0], qb[2 * j + i][1]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[i] += y[i];
+    };
     int stage = 0;
+    if (tile < n_tiles) {
+        ptx::cp_async_wait<C::NS - 1>();
+        __syncwarp();
+        products(ring + (C::NS - 1) * 2 * C::HALF);
+    }
 
     for (; tile < n_tiles; tile += step) {
         const uint32_t valid = __ballot_sync(0xffffffffu, slot >= 0);
+        // every row that this tile copies has a slot
+        const bool whole = __all_sync(0xffffffffu, (slot1 | slot2) >= 0) && valid == 0xffffffffu;
         scales_of(slot1, ks1, vs1);
-        const float lv = E4M3 ? __log2f(fmaxf(vs, 1e-37f)) : 0.f;
+        const float lv = E4M3 ? __log2f(fmaxf(vs, 1e-37f)) : 0.f, kfac = ks * factor;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             if (half == 1 && tile * 32 + 16 >= n) break;
-            ptx::cp_async_wait<C::NS - 2>();
             __syncwarp();
             {   // the stage read last takes the one NS - 1 further on
                 const int to = stage == 0 ? C::NS - 1 : stage - 1;
-                if (C::NS == 2 && half == 0) copy_stage(to, slot, 1);
-                else copy_stage(to, slot1, C::NS == 2 ? 0 : half);
+                const int32_t ksl = C::NS == 2 || half == 0 ? slot1 : slot2;
+                const int kh = C::NS == 2 ? half : 1 - half;
+                if (whole) {
+                    copy_v(to, full);
+                    copy_k(to, ksl, kh, full);
+                } else {
+                    copy_v(to, some);
+                    copy_k(to, ksl, kh, some);
+                }
                 ptx::cp_async_commit();
             }
-            const char* st = ring + stage * 2 * C::HALF;
-            stage = stage == C::NS - 1 ? 0 : stage + 1;
-
-            // ---- logits: keys r8, r8 + 8; heads 2 t4, 2 t4 + 1 ----
-            float z[4] = {0.f, 0.f, 0.f, 0.f};
+            // ---- logits, less their references ----
+            float d1[4], d2[4], ev[2] = {0.f, 0.f}, kf[2] = {factor, factor};
 #pragma unroll
-            for (int j = 0; j < C::KW / 4; ++j) {
-                // chunk 4 j + t4: bit 6 of the offset is j's lowest bit, XORed
-                const char* p = st + ((k_at + (j >> 1) * 128) ^ ((j & 1) << 6));
-                const uint4 x = *reinterpret_cast<const uint4*>(p);
-                const uint4 y = *reinterpret_cast<const uint4*>(p + 8 * C::ROWB);
-                const uint32_t k0[4] = {x.x, x.y, x.z, x.w}, k1[4] = {y.x, y.y, y.z, y.w};
+            for (int u = 0; u < 2; ++u)
                 if (E4M3) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        mma_f16_16816(z, lo_f16x2(k0[i]), lo_f16x2(k1[i]), hi_f16x2(k0[i]),
-                                      hi_f16x2(k1[i]), qb[4 * j + i][0], qb[4 * j + i][1]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        ptx::mma_bf16_16816(z, k0[2 * i], k1[2 * i], k0[2 * i + 1], k1[2 * i + 1],
-                                            qb[2 * j + i][0], qb[2 * j + i][1]);
-                }
-            }
-            float ev[2] = {0.f, 0.f};
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                if (E4M3) {
-                    const float kf = __shfl_sync(0xffffffffu, ks, half * 16 + u * 8 + r8);
+                    kf[u] = __shfl_sync(0xffffffffu, kfac, half * 16 + u * 8 + r8);
                     ev[u] = __shfl_sync(0xffffffffu, lv, half * 16 + u * 8 + r8);
-                    z[2 * u] *= kf * cq[0];
-                    z[2 * u + 1] *= kf * cq[1];
-                } else {
-                    z[2 * u] *= cq[0];
-                    z[2 * u + 1] *= cq[1];
                 }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                d1[i] = fmaf(z[i], kf[i >> 1], -m1[i & 1]);
+                d2[i] = E4M3 ? fmaf(z[i], kf[i >> 1], ev[i >> 1] - m2[i & 1]) : d1[i];
             }
             if (valid != 0xffffffffu) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (!(valid >> (half * 16 + (i >> 1) * 8 + r8) & 1)) z[i] = -INFINITY;
+                    if (!(valid >> (half * 16 + (i >> 1) * 8 + r8) & 1)) d1[i] = d2[i] = -INFINITY;
             }
-            bool over = false;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                over |= z[i] > m1[i & 1] + PT_SLACK;
-                if (E4M3) over |= z[i] + ev[i >> 1] > m2[i & 1] + PT_SLACK;
-            }
-            if (__any_sync(0xffffffffu, over)) {
+            float top = fmaxf(fmaxf(d1[0], d1[1]), fmaxf(d1[2], d1[3]));
+            if (E4M3) top = fmaxf(top, fmaxf(fmaxf(d2[0], d2[1]), fmaxf(d2[2], d2[3])));
+            if (__any_sync(0xffffffffu, top > PT_SLACK)) {
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    float x1 = fmaxf(m1[c], fmaxf(z[c], z[2 + c]));
-                    float x2 = fmaxf(m2[c], fmaxf(z[c] + ev[0], z[2 + c] + ev[1]));
+                    float n1 = m1[c], n2 = m2[c];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+                        if (d1[2 * u + c] > -INFINITY) {
+                            const float x = z[2 * u + c] * kf[u];
+                            n1 = fmaxf(n1, x);
+                            n2 = fmaxf(n2, x + ev[u]);
+                        }
 #pragma unroll
                     for (int o = 4; o <= 16; o <<= 1) {
-                        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, o));
-                        if (E4M3) x2 = fmaxf(x2, __shfl_xor_sync(0xffffffffu, x2, o));
+                        n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, o));
+                        if (E4M3) n2 = fmaxf(n2, __shfl_xor_sync(0xffffffffu, n2, o));
                     }
-                    if (!E4M3) x2 = x1;
-                    const float f2 = ex2(m2[c] - x2);
-                    l[c] *= ex2(m1[c] - x1);
-                    m1[c] = x1;
-                    m2[c] = x2;
+                    if (!E4M3) n2 = n1;
+                    const float f2 = ex2(m2[c] - n2);
+                    l[c] *= ex2(m1[c] - n1);
+                    m1[c] = n1;
+                    m2[c] = n2;
 #pragma unroll
                     for (int j = 0; j < C::DT; ++j) {
                         acc[j][c] *= f2;
                         acc[j][c + 2] *= f2;
+                    }
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const int i = 2 * u + c;
+                        const bool none = d1[i] == -INFINITY;
+                        d1[i] = none ? -INFINITY : fmaf(z[i], kf[u], -n1);
+                        d2[i] = none ? -INFINITY : fmaf(z[i], kf[u], ev[u] - n2);
                     }
                 }
             }
@@ -382,12 +449,11 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
             uint32_t pb[2], pl[2];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const float x0 = z[2 * u], x1 = z[2 * u + 1];
-                const float p0 = ex2(x0 - m1[0]), p1 = ex2(x1 - m1[1]);
+                const float p0 = ex2(d1[2 * u]), p1 = ex2(d1[2 * u + 1]);
                 l[0] += p0;
                 l[1] += p1;
                 if (E4M3) {
-                    pb[u] = ptx::movmatrix_t(pack_f16(ex2(x0 + ev[u] - m2[0]), ex2(x1 + ev[u] - m2[1])));
+                    pb[u] = ptx::movmatrix_t(pack_f16(ex2(d2[2 * u]), ex2(d2[2 * u + 1])));
                 } else {
                     const uint32_t hi = ptx::pack_bf16(p0, p1);
                     pb[u] = ptx::movmatrix_t(hi);
@@ -395,6 +461,11 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
                                                             p1 - __uint_as_float(hi & 0xffff0000u)));
                 }
             }
+            ptx::cp_async_wait<C::NS - 1>();
+            __syncwarp();
+            const char* st = ring + stage * 2 * C::HALF;
+            stage = stage == C::NS - 1 ? 0 : stage + 1;
+            products(st);                               // of the next 16 keys
             // ---- O^T += V^T P: keys 2 t4, 2 t4 + 1, 2 t4 + 8, 2 t4 + 9 ----
             uint32_t vw[4][C::VW];
 #pragma unroll
@@ -423,16 +494,15 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
                 const uint32_t r0 = vw[0][w], r1 = vw[1][w], r2 = vw[2][w], r3 = vw[3][w];
                 if (E4M3) {
                     const uint32_t x = __byte_perm(r0, r1, 0x5140), y = __byte_perm(r2, r3, 0x5140);
-                    mma_f16_16816(acc[2 * w], lo_f16x2(x), hi_f16x2(x), lo_f16x2(y), hi_f16x2(y),
-                                  pb[0], pb[1]);
+                    mma_f16(acc[2 * w], lo_f16x2(x), hi_f16x2(x), lo_f16x2(y), hi_f16x2(y), pb[0], pb[1]);
                     const uint32_t x2 = __byte_perm(r0, r1, 0x7362), y2 = __byte_perm(r2, r3, 0x7362);
-                    mma_f16_16816(acc[2 * w + 1], lo_f16x2(x2), hi_f16x2(x2), lo_f16x2(y2),
-                                  hi_f16x2(y2), pb[0], pb[1]);
+                    mma_f16(acc[2 * w + 1], lo_f16x2(x2), hi_f16x2(x2), lo_f16x2(y2), hi_f16x2(y2),
+                            pb[0], pb[1]);
                 } else {
                     const uint32_t a0 = __byte_perm(r0, r1, 0x5410), a1 = __byte_perm(r0, r1, 0x7632);
                     const uint32_t a2 = __byte_perm(r2, r3, 0x5410), a3 = __byte_perm(r2, r3, 0x7632);
-                    ptx::mma_bf16_16816(acc[w], a0, a1, a2, a3, pb[0], pb[1]);
-                    ptx::mma_bf16_16816(acc[w], a0, a1, a2, a3, pl[0], pl[1]);
+                    mma_bf16(acc[w], a0, a1, a2, a3, pb[0], pb[1]);
+                    mma_bf16(acc[w], a0, a1, a2, a3, pl[0], pl[1]);
                 }
             }
         }
@@ -571,9 +641,14 @@ cudaError_t launch_paged_attn(const lsa_paged_kv& kv, const void* Q, int64_t Nq,
     a.O = (__nv_bfloat16*)O;
     a.lse = lse;
     const int64_t units = kv.B * Nq * kv.Hkv * a.chunks;
-    // CTAs per unit: enough to fill the SMs, each with at least a tile per warp
+    // CTAs per unit: as many as are resident at once, each with a tile per warp at
+    // least.  16 leave too few places in the GPCs once the grid is over a quarter
+    // of the device (8 sequences of 4 units: 16.7 us with 8, 22.5 us with 16).
+    const int64_t slots = (int64_t)sm_count() * (kv.format == LSA_KV_BF16 && kv.d == 128 ? 3 : 4);
     int c = 1;
-    while (c < PT_MAX_C && units * c * 2 <= 4 * 148 && s_max >= 2 * c * PT_WARPS * 32) c *= 2;
+    while (c < PT_MAX_C && units * c * 2 <= (c == 8 ? slots / 4 : slots) &&
+           s_max >= 2 * c * PT_WARPS * 32)
+        c *= 2;
     auto run = [&](auto kern, int bytes) {
         cudaError_t e = ensure_smem_attr((const void*)kern, bytes);
         if (e == cudaSuccess && c > 8)
