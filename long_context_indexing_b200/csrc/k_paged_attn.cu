@@ -10,11 +10,12 @@
 // and no warp waits for another until the end.  Keys are the M side of both
 // products and the query heads the N side of 8, so that a group of 8 heads
 // fills the warp MMA: S[key][head] = K Q^T, O^T[dim][head] += V^T P.
-//   * A lane looks up one key of a tile: its position two tiles before the page
-//     table's entry is needed, the entry a tile before the rows are asked for,
-//     the rows brought to L2 two tiles ahead and to the warp's own ring of
-//     16-key stages in shared memory (16-byte asynchronous copies) one to two
-//     stages ahead.
+//   * A lane looks up one key of a tile.  Positions, page table entries, scales
+//     and rows all come by asynchronous copies into the warp's own rings in
+//     shared memory, requested two tiles (rows: one to two stages of 16 keys)
+//     before they are used, so that nothing in the loop waits for a load by
+//     name: with loads to registers in their place the warps spent over a third
+//     of their time at them.
 //   * A lane takes 16 consecutive bytes of a K row as fragment elements, which
 //     only renames the contraction index (Q's fragments are renamed alike), and
 //     of V rows, which renames the output rows; V's pairs along the keys are
@@ -67,9 +68,13 @@ struct PagedCfg {
     static constexpr int HALF = 16 * ROWB;            // bytes of a stage's K (or V)
     static constexpr int RING = NS * 2 * HALF;        // bytes of a warp's ring
     static constexpr int EPT = PT_H * D / PT_THREADS; // merged elements per thread
-    // the cluster's slices and the CTAs' references and sums
-    static constexpr int RECV = PT_H * D, RECV_ML = 3 * PT_H * PT_MAX_C;
-    static constexpr int BYTES = PT_WARPS * RING + 4 * (RECV + RECV_ML + 3 * PT_WARPS * PT_H);
+    // a warp's positions [4][32], pages [2][32] and scales [4][2][32] of tiles
+    static constexpr int META = 4 * 32 * (E4M3 ? 4 + 2 + 8 : 4 + 2);
+    static constexpr int BYTES = PT_WARPS * (RING + META) + 4 * 3 * PT_WARPS * PT_H;
+    // after the loop: O^T of a warp at its ring, the cluster's slices behind the
+    // first warp's, the CTAs' references and sums in place of the positions
+    static constexpr int RECV = 4 * PT_H * D;
+    static_assert(2 * RECV <= RING && 4 * 3 * PT_H * PT_MAX_C <= PT_WARPS * META, "merge arrays fit");
 };
 
 struct PagedAttnArgs {
@@ -85,9 +90,11 @@ struct PagedAttnArgs {
     float* lse;
 };
 
-__device__ __forceinline__ void prefetch_l2(const void* p)
+// 4 bytes to shared memory.
+__device__ __forceinline__ void copy4(void* dst, const void* src)
 {
-    asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(ptx::smem_addr(dst)), "l"(src)
+                 : "memory");
 }
 __device__ __forceinline__ float ex2(float x)
 {
@@ -159,14 +166,12 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
 {
     using C = PagedCfg<E4M3, D>;
     extern __shared__ __align__(128) char smem[];
-    float* recv = reinterpret_cast<float*>(smem + PT_WARPS * C::RING);
-    float* recv_ml = recv + C::RECV;                   // [CTA][m1, m2, l][head]
-    float* ml_s = recv_ml + C::RECV_ML;                // [warp][m1, m2, l][head]
+    float* recv = reinterpret_cast<float*>(smem + C::RECV);
+    float* recv_ml = reinterpret_cast<float*>(smem + PT_WARPS * C::RING);   // [CTA][m1, m2, l][head]
+    float* ml_s = reinterpret_cast<float*>(smem + PT_WARPS * (C::RING + C::META));   // [warp] likewise
     uint32_t rank, n_cta;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(n_cta));
-    // the CTAs of the cluster have started before any is written to
-    if (n_cta > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r8 = lane >> 2, t4 = lane & 3;
     const int64_t unit = blockIdx.x / n_cta;
@@ -180,7 +185,7 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
     const int n = min(max(__ldg(a.counts + row), 0), a.s_max);
     const int32_t* idx = a.indices + row * a.s_max;
     const int32_t* table = kv.page_table + b * kv.max_pages;
-    const int32_t t_end = (int32_t)(kv.max_pages << a.page_shift);
+    const uint32_t t_end = (uint32_t)(kv.max_pages << a.page_shift);
     const uint32_t tok_bytes = (uint32_t)kv.Hkv * C::ROWB;
     const char* Kb = (const char*)kv.K + (int64_t)g * C::ROWB;
     const char* Vb = (const char*)kv.V + (int64_t)g * C::ROWB;
@@ -188,41 +193,31 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
     const int step = (int)n_cta * PT_WARPS;
     int tile = (int)rank * PT_WARPS + warp;
 
-    // position of this lane's key of a tile, its page, its slot (-1: none).  A
-    // page is looked at one tile after its look-up.
-    // (positions are asked for before the row's count is known)
-    auto position = [&](int ti) {
-        const int k = ti * 32 + lane;
-        return k < a.s_max ? __ldg(idx + k) : -1;
-    };
+    // position of this lane's key of tile ti, its page table entry; both clamped
+    // into their arrays and checked with the slot (-1: none)
+    auto position = [&](int ti) { return idx + min(ti * 32 + lane, a.s_max - 1); };
     auto page = [&](int32_t t) {
-        return (uint32_t)t < (uint32_t)t_end ? __ldg(table + (t >> a.page_shift)) : -1;
+        return table + min((uint32_t)t >> a.page_shift, (uint32_t)kv.max_pages - 1u);
     };
     auto slot_of = [&](int32_t t, int32_t pg, int ti) {
         if (ti * 32 + lane >= n) return -1;
-        if ((uint32_t)pg >= (uint32_t)kv.n_pages) {
+        if ((uint32_t)t >= t_end || (uint32_t)pg >= (uint32_t)kv.n_pages) {
             dev_error(kv.status, DEV_BAD_PAGE, (uint32_t)t);
             return -1;
         }
         return (pg << a.page_shift) + (t & (kv.page - 1));
     };
-    // brings this lane's key's rows into L2
-    auto prefetch = [&](int32_t slot) {
-        if (slot < 0) return;
-        const uint64_t off = (uint64_t)(uint32_t)slot * tok_bytes;
-#pragma unroll
-        for (int x = 0; x < C::ROWB; x += 128) {
-            prefetch_l2(Kb + off + x);
-            prefetch_l2(Vb + off + x);
-        }
-    };
-    float ks = 0.f, vs = 0.f, ks1 = 0.f, vs1 = 0.f;     // scales of a tile's keys, and the next's
-    auto scales_of = [&](int32_t slot, float& k, float& v) {
-        k = v = 0.f;
-        if (E4M3 && slot >= 0) {
-            const float* s = kv.scales + (int64_t)(slot / SCALE_BLOCK) * (2 * kv.Hkv) + g;
-            k = __ldg(s);
-            v = __ldg(s + kv.Hkv);
+    char* meta = smem + PT_WARPS * C::RING + warp * C::META;
+    int32_t* pos_s = reinterpret_cast<int32_t*>(meta) + lane;          // [4][32]
+    int32_t* page_s = pos_s + 4 * 32;                                  // [2][32]
+    float* scale_s = reinterpret_cast<float*>(meta) + 6 * 32;          // [4][keys', values'][32]
+    // (of slot 0 for a key without a slot, whose logit is replaced)
+    auto copy_scales = [&](int at, int32_t slot) {
+        if (E4M3) {
+            const float* s = kv.scales + (uint64_t)((uint32_t)max(slot, 0) / SCALE_BLOCK) *
+                                             (uint32_t)(2 * kv.Hkv) + g;
+            copy4(scale_s + at * 64 + lane, s);
+            copy4(scale_s + at * 64 + 32 + lane, s + kv.Hkv);
         }
     };
     // A stage of the ring: V of 16 keys, K of the 16 after them; keys without a
@@ -263,27 +258,27 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
         if (r8 < nh) qw[s] = __ldg(reinterpret_cast<const uint2*>(a.Q + (hbase + r8) * D + c));
     }
 
-    // the first tiles: in the loop, slot is the tile's, slot1 and slot2 the next
-    // two tiles' (slot2's rows on their way to L2), pos3 / pg3 and pos4 look two
-    // tiles further
-    int32_t slot = -1, slot1 = -1, slot2 = -1, pos3 = -1, pg3 = -1, pos4 = -1;
-    if (tile * 32 < a.s_max) {
-        const int32_t p0 = position(tile), p1 = position(tile + step), p2 = position(tile + 2 * step);
-        pos3 = position(tile + 3 * step);
-        pos4 = position(tile + 4 * step);
-        const int32_t g0 = page(p0), g1 = page(p1), g2 = page(p2);
-        pg3 = page(pos3);
+    // the first tiles: in the loop, slot, slot1, slot2 are the tile's and the next
+    // two tiles'; the positions of the three after those are asked for, and the
+    // pages of the first of them
+    int32_t slot = -1, slot1 = -1, slot2 = -1;
+    if (tile < n_tiles) {
+        const int32_t p0 = __ldg(position(tile)), p1 = __ldg(position(tile + step));
+        const int32_t p2 = __ldg(position(tile + 2 * step)), p3 = __ldg(position(tile + 3 * step));
+#pragma unroll
+        for (int x = 3; x < 6; ++x) copy4(pos_s + (x & 3) * 32, position(tile + x * step));
+        const int32_t g0 = __ldg(page(p0)), g1 = __ldg(page(p1)), g2 = __ldg(page(p2));
         slot = slot_of(p0, g0, tile);
-        scales_of(slot, ks, vs);
+        copy_scales(0, slot);
         copy_k(C::NS - 1, slot, 0, some);
         ptx::cp_async_commit();
         copy_v(0, some);
         copy_k(0, slot, 1, some);
-        ptx::cp_async_commit();
         slot1 = slot_of(p1, g1, tile + step);
         slot2 = slot_of(p2, g2, tile + 2 * step);
-        prefetch(slot1);
-        prefetch(slot2);
+        copy4(page_s + 32, page(p3));
+        copy_scales(1, slot1);
+        ptx::cp_async_commit();
         if (C::NS > 2) {
             copy_v(1, some);
             copy_k(1, slot1, 0, some);
@@ -367,12 +362,10 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
         products(ring + (C::NS - 1) * 2 * C::HALF);
     }
 
-    for (; tile < n_tiles; tile += step) {
+    for (int it = 0; tile < n_tiles; tile += step, ++it) {
         const uint32_t valid = __ballot_sync(0xffffffffu, slot >= 0);
         // every row that this tile copies has a slot
         const bool whole = __all_sync(0xffffffffu, (slot1 | slot2) >= 0) && valid == 0xffffffffu;
-        scales_of(slot1, ks1, vs1);
-        const float lv = E4M3 ? __log2f(fmaxf(vs, 1e-37f)) : 0.f, kfac = ks * factor;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             if (half == 1 && tile * 32 + 16 >= n) break;
@@ -381,6 +374,11 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
                 const int to = stage == 0 ? C::NS - 1 : stage - 1;
                 const int32_t ksl = C::NS == 2 || half == 0 ? slot1 : slot2;
                 const int kh = C::NS == 2 ? half : 1 - half;
+                if (half == 0) {
+                    copy4(pos_s + ((it + 6) & 3) * 32, position(tile + 6 * step));
+                    copy4(page_s + (it & 1) * 32, page(pos_s[(it & 3) * 32]));   // tile it + 4
+                    copy_scales((it + 2) & 3, slot2);
+                }
                 if (whole) {
                     copy_v(to, full);
                     copy_k(to, ksl, kh, full);
@@ -395,8 +393,9 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
 #pragma unroll
             for (int u = 0; u < 2; ++u)
                 if (E4M3) {
-                    kf[u] = __shfl_sync(0xffffffffu, kfac, half * 16 + u * 8 + r8);
-                    ev[u] = __shfl_sync(0xffffffffu, lv, half * 16 + u * 8 + r8);
+                    const float* s = scale_s + (it & 3) * 64 + half * 16 + u * 8 + r8;
+                    kf[u] *= s[0];
+                    ev[u] = __log2f(fmaxf(s[32], 1e-37f));
                 }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -507,19 +506,14 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
             }
         }
         slot = slot1;
-        ks = ks1;
-        vs = vs1;
         slot1 = slot2;
-        slot2 = slot_of(pos3, pg3, tile + 3 * step);
-        prefetch(slot2);
-        pos3 = pos4;
-        pg3 = page(pos3);
-        pos4 = position(tile + 5 * step);
+        slot2 = slot_of(pos_s[((it + 3) & 3) * 32], page_s[((it + 3) & 1) * 32], tile + 3 * step);
     }
 
     // ---- merge: lanes, warps, CTAs ----
     ptx::cp_async_wait<0>();
-    __syncwarp();                                       // the ring is free
+    __syncwarp();                                       // the rings are free
+    if (n_cta > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     float* o_s = reinterpret_cast<float*>(smem);        // warp w's O^T at w * RING
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
@@ -566,7 +560,8 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
         for (int i = 0; i < C::EPT; ++i) o[i] += f * src[i * 64];
     }
     if (n_cta > 1) {
-        asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+        // every CTA's rings are free
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
         // thread t's elements go to CTA t / tpc, place (source CTA, t % tpc)
         const uint32_t tpc = PT_THREADS / n_cta;
         const uint32_t to = threadIdx.x / tpc, at = threadIdx.x % tpc;
