@@ -12,10 +12,10 @@
 // fills the warp MMA: S[key][head] = K Q^T, O^T[dim][head] += V^T P.
 //   * A lane looks up one key of a tile.  Positions, page table entries, scales
 //     and rows all come by asynchronous copies into the warp's own rings in
-//     shared memory, requested two tiles (rows: one to two stages of 16 keys)
-//     before they are used, so that nothing in the loop waits for a load by
-//     name: with loads to registers in their place the warps spent over a third
-//     of their time at them.
+//     shared memory, each asked for a tile (rows: a stage of 16 keys) before it
+//     is used, so that nothing in the loop waits for a load by name: with loads
+//     to registers in their place the warps spent over a third of their time at
+//     them.  Rings three deep are no faster.
 //   * A lane takes 16 consecutive bytes of a K row as fragment elements, which
 //     only renames the contraction index (Q's fragments are renamed alike), and
 //     of V rows, which renames the output rows; V's pairs along the keys are
@@ -63,13 +63,13 @@ struct PagedCfg {
     static constexpr int LPR = ROWB / 16;             // lanes (16-byte chunks) per row
     static constexpr int RPI = 32 / LPR;              // rows per warp copy
     static constexpr int RI = 16 / RPI;               // copies of 16 rows
-    static constexpr int NS = ROWB > 128 ? 2 : 3;     // stages of a warp's ring
     static constexpr int MINB = ROWB > 128 ? 3 : 4;   // CTAs per SM
     static constexpr int HALF = 16 * ROWB;            // bytes of a stage's K (or V)
-    static constexpr int RING = NS * 2 * HALF;        // bytes of a warp's ring
+    static constexpr int STAGE = 2 * HALF;
+    static constexpr int RING = 2 * STAGE;            // bytes of a warp's ring
     static constexpr int EPT = PT_H * D / PT_THREADS; // merged elements per thread
-    // a warp's positions [4][32], pages [2][32] and scales [4][2][32] of tiles
-    static constexpr int META = 4 * 32 * (E4M3 ? 4 + 2 + 8 : 4 + 2);
+    // a warp's positions [2][32], pages [32] and scales [2][2][32] of tiles
+    static constexpr int META = 4 * 32 * (E4M3 ? 2 + 1 + 4 : 2 + 1);
     static constexpr int BYTES = PT_WARPS * (RING + META) + 4 * 3 * PT_WARPS * PT_H;
     // after the loop: O^T of a warp at its ring, the cluster's slices behind the
     // first warp's, the CTAs' references and sums in place of the positions
@@ -208,9 +208,9 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
         return (pg << a.page_shift) + (t & (kv.page - 1));
     };
     char* meta = smem + PT_WARPS * C::RING + warp * C::META;
-    int32_t* pos_s = reinterpret_cast<int32_t*>(meta) + lane;          // [4][32]
-    int32_t* page_s = pos_s + 4 * 32;                                  // [2][32]
-    float* scale_s = reinterpret_cast<float*>(meta) + 6 * 32;          // [4][keys', values'][32]
+    int32_t* pos_s = reinterpret_cast<int32_t*>(meta) + lane;          // [2][32]
+    int32_t* page_s = pos_s + 2 * 32;                                  // [32]
+    float* scale_s = reinterpret_cast<float*>(meta) + 3 * 32;          // [2][keys', values'][32]
     // (of slot 0 for a key without a slot, whose logit is replaced)
     auto copy_scales = [&](int at, int32_t slot) {
         if (E4M3) {
@@ -234,7 +234,7 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
     auto copy_v = [&](int stage, auto full) {
 #pragma unroll
         for (int i = 0; i < C::RI; ++i)
-            copy16<decltype(full)::value>((vc_at ^ ((i * C::RPI & 6) << 4)) + stage * 2 * C::HALF +
+            copy16<decltype(full)::value>((vc_at ^ ((i * C::RPI & 6) << 4)) + stage * C::STAGE +
                                               i * C::RPI * C::ROWB,
                                           Vc, rs[i], tok_bytes);
     };
@@ -242,7 +242,7 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
 #pragma unroll
         for (int i = 0; i < C::RI; ++i) {
             rs[i] = __shfl_sync(0xffffffffu, slot, half * 16 + i * C::RPI + crow);
-            copy16<decltype(full)::value>(kc_at + stage * 2 * C::HALF + i * C::RPI * C::ROWB, Kc, rs[i],
+            copy16<decltype(full)::value>(kc_at + stage * C::STAGE + i * C::RPI * C::ROWB, Kc, rs[i],
                                           tok_bytes);
         }
     };
@@ -258,32 +258,22 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
         if (r8 < nh) qw[s] = __ldg(reinterpret_cast<const uint2*>(a.Q + (hbase + r8) * D + c));
     }
 
-    // the first tiles: in the loop, slot, slot1, slot2 are the tile's and the next
-    // two tiles'; the positions of the three after those are asked for, and the
-    // pages of the first of them
-    int32_t slot = -1, slot1 = -1, slot2 = -1;
+    // the first tile: in the loop, slot and slot1 are the tile's and the next
+    // one's, whose positions and pages have been; the position after them is
+    // asked for
+    int32_t slot = -1, slot1 = -1;
     if (tile < n_tiles) {
         const int32_t p0 = __ldg(position(tile)), p1 = __ldg(position(tile + step));
-        const int32_t p2 = __ldg(position(tile + 2 * step)), p3 = __ldg(position(tile + 3 * step));
-#pragma unroll
-        for (int x = 3; x < 6; ++x) copy4(pos_s + (x & 3) * 32, position(tile + x * step));
-        const int32_t g0 = __ldg(page(p0)), g1 = __ldg(page(p1)), g2 = __ldg(page(p2));
+        copy4(pos_s, position(tile + 2 * step));
+        const int32_t g0 = __ldg(page(p0)), g1 = __ldg(page(p1));
         slot = slot_of(p0, g0, tile);
         copy_scales(0, slot);
-        copy_k(C::NS - 1, slot, 0, some);
+        copy_k(1, slot, 0, some);
         ptx::cp_async_commit();
         copy_v(0, some);
         copy_k(0, slot, 1, some);
-        slot1 = slot_of(p1, g1, tile + step);
-        slot2 = slot_of(p2, g2, tile + 2 * step);
-        copy4(page_s + 32, page(p3));
-        copy_scales(1, slot1);
         ptx::cp_async_commit();
-        if (C::NS > 2) {
-            copy_v(1, some);
-            copy_k(1, slot1, 0, some);
-            ptx::cp_async_commit();
-        }
+        slot1 = slot_of(p1, g1, tile + step);
     }
 
     uint32_t qb[C::KS][2];                              // Q fragments
@@ -355,36 +345,33 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
 #pragma unroll
         for (int i = 0; i < 4; ++i) z[i] += y[i];
     };
-    int stage = 0;
     if (tile < n_tiles) {
-        ptx::cp_async_wait<C::NS - 1>();
+        ptx::cp_async_wait<1>();
         __syncwarp();
-        products(ring + (C::NS - 1) * 2 * C::HALF);
+        products(ring + C::STAGE);
     }
 
     for (int it = 0; tile < n_tiles; tile += step, ++it) {
         const uint32_t valid = __ballot_sync(0xffffffffu, slot >= 0);
         // every row that this tile copies has a slot
-        const bool whole = __all_sync(0xffffffffu, (slot1 | slot2) >= 0) && valid == 0xffffffffu;
+        const bool whole = __all_sync(0xffffffffu, slot1 >= 0) && valid == 0xffffffffu;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             if (half == 1 && tile * 32 + 16 >= n) break;
             __syncwarp();
-            {   // the stage read last takes the one NS - 1 further on
-                const int to = stage == 0 ? C::NS - 1 : stage - 1;
-                const int32_t ksl = C::NS == 2 || half == 0 ? slot1 : slot2;
-                const int kh = C::NS == 2 ? half : 1 - half;
+            {   // the stage read last takes the next one: V of the 16 keys after
+                // these, K of the 16 after those
                 if (half == 0) {
-                    copy4(pos_s + ((it + 6) & 3) * 32, position(tile + 6 * step));
-                    copy4(page_s + (it & 1) * 32, page(pos_s[(it & 3) * 32]));   // tile it + 4
-                    copy_scales((it + 2) & 3, slot2);
+                    copy4(pos_s + ((it + 1) & 1) * 32, position(tile + 3 * step));
+                    copy4(page_s, page(pos_s[(it & 1) * 32]));       // two tiles on
+                    copy_scales((it + 1) & 1, slot1);
                 }
                 if (whole) {
-                    copy_v(to, full);
-                    copy_k(to, ksl, kh, full);
+                    copy_v(1 - half, full);
+                    copy_k(1 - half, slot1, half, full);
                 } else {
-                    copy_v(to, some);
-                    copy_k(to, ksl, kh, some);
+                    copy_v(1 - half, some);
+                    copy_k(1 - half, slot1, half, some);
                 }
                 ptx::cp_async_commit();
             }
@@ -393,7 +380,7 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
 #pragma unroll
             for (int u = 0; u < 2; ++u)
                 if (E4M3) {
-                    const float* s = scale_s + (it & 3) * 64 + half * 16 + u * 8 + r8;
+                    const float* s = scale_s + (it & 1) * 64 + half * 16 + u * 8 + r8;
                     kf[u] *= s[0];
                     ev[u] = __log2f(fmaxf(s[32], 1e-37f));
                 }
@@ -460,10 +447,9 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
                                                             p1 - __uint_as_float(hi & 0xffff0000u)));
                 }
             }
-            ptx::cp_async_wait<C::NS - 1>();
+            ptx::cp_async_wait<1>();
             __syncwarp();
-            const char* st = ring + stage * 2 * C::HALF;
-            stage = stage == C::NS - 1 ? 0 : stage + 1;
+            const char* st = ring + half * C::STAGE;
             products(st);                               // of the next 16 keys
             // ---- O^T += V^T P: keys 2 t4, 2 t4 + 1, 2 t4 + 8, 2 t4 + 9 ----
             uint32_t vw[4][C::VW];
@@ -506,8 +492,7 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
             }
         }
         slot = slot1;
-        slot1 = slot2;
-        slot2 = slot_of(pos_s[((it + 3) & 3) * 32], page_s[((it + 3) & 1) * 32], tile + 3 * step);
+        slot1 = slot_of(pos_s[(it & 1) * 32], page_s[0], tile + 2 * step);
     }
 
     // ---- merge: lanes, warps, CTAs ----
