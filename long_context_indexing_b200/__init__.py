@@ -712,12 +712,15 @@ class LsaPagedKV:
             _check(_lib.lsa_paged_check(self._ref, _stream(stream)))
 
 
+_BF16, _I32 = torch.bfloat16, torch.int32
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _elsewhere(cache, stream):
-    """None when the cache's device is current and no stream is given, else the context that
-    makes that device (and stream) current, so that launches and new tensors belong to them."""
+    """The context that makes the cache's device (and `stream`) current, so that launches and
+    new tensors belong to them."""
     if stream is None:
-        if torch._C._cuda_getDevice() == cache._index:
-            return None
         return torch.cuda.device(cache.device)
     if stream.device != cache.device:
         raise ValueError("the stream is on another device")
@@ -731,7 +734,7 @@ def _same_device(device, *ts):
 
 
 def _int32(cache, t, what, shape):
-    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous() or \
+    if t.shape != shape or t.dtype is not _I32 or not t.is_contiguous() or \
             t.get_device() != cache._index:
         raise TypeError("%s must be a contiguous int32 tensor of shape %s on %s"
                         % (what, shape, cache.device))
@@ -740,14 +743,16 @@ def _int32(cache, t, what, shape):
 def _rows(cache, t, what, B, Nq, H):
     """Elements between consecutive token rows of a bfloat16 [B][Nq][H][d] tensor whose rows
     are contiguous (a slice of a wider projection, for instance); H None: any."""
-    if t.dtype is not torch.bfloat16 or t.dim() != 4 or t.get_device() != cache._index:
+    if t.dtype is not _BF16 or t.get_device() != cache._index or t.dim() != 4:
         raise TypeError("%s must be a bfloat16 tensor [B][Nq][heads][d] on %s"
                         % (what, cache.device))
     b, n, h, d = t.shape
-    sb, sn, sh, se = t.stride()
-    if b != B or n != Nq or d != cache.d or (H is not None and h != H):
+    if b != B or n != Nq or d != cache.d or (h != H and H is not None):
         raise ValueError("%s has shape %s, not [%d][%d][%s][%d]"
                          % (what, tuple(t.shape), B, Nq, "heads" if H is None else H, cache.d))
+    if t.is_contiguous():
+        return h * d
+    sb, sn, sh, se = t.stride()
     row = sn if n > 1 else (sb if b > 1 else h * d)
     if se != 1 or (sh != d and h > 1) or (sb != n * row and b > 1 and n > 0):
         raise ValueError("%s must have contiguous rows at one distance (strides %s)"
@@ -757,7 +762,7 @@ def _rows(cache, t, what, B, Nq, H):
 
 def _like(cache, t, what, shape):
     """A contiguous bfloat16 tensor of `shape` on the cache's device."""
-    if t.dtype is not torch.bfloat16 or t.shape != shape or not t.is_contiguous() or \
+    if t.shape != shape or t.dtype is not _BF16 or not t.is_contiguous() or \
             t.get_device() != cache._index:
         raise TypeError("%s must be a contiguous bfloat16 tensor of shape %s on %s"
                         % (what, tuple(shape), cache.device))
@@ -770,9 +775,8 @@ def lsa_paged_append(cache, k, v, start, n_new=None, q=None, q_out=None, inv_fre
     rotation); tokens at and after n_new[b] are padding.  With q [B][Nq][Hq][d] the queries are
     rotated too: into q_out (which may be q; rows of padding are left as they are) or a new
     tensor, which is returned (None without q).  C: lsa_paged_append."""
-    ctx = _elsewhere(cache, stream)
-    if ctx is not None:
-        with ctx:
+    if stream is not None or _current_device() != cache._index:
+        with _elsewhere(cache, stream):
             return lsa_paged_append(cache, k, v, start, n_new, q, q_out, inv_freq, interleaved)
     B, Nq = cache.B, k.shape[1]
     ks = _rows(cache, k, "k", B, Nq, cache.Hkv)
@@ -802,7 +806,7 @@ def lsa_paged_append(cache, k, v, start, n_new=None, q=None, q_out=None, inv_fre
         None if q is None else q_out.data_ptr(), Nq, Hq, start.data_ptr(),
         None if n_new is None else n_new.data_ptr(),
         None if inv_freq is None else inv_freq.data_ptr(), rot, bool(interleaved),
-        torch._C._cuda_getCurrentRawStream(cache._index)))
+        _raw_stream(cache._index)))
     return q_out
 
 
@@ -811,9 +815,8 @@ def lsa_paged_attn(cache, Q, indices, counts, scale=None, return_lse=False, out=
     """Attention of Q [B][Nq][Hq][d] (bfloat16) over the listed positions of the paged cache
     (C: lsa_paged_attn): indices [B][Nq][s_max], counts [B][Nq] int32, as the selections return
     them.  A row of count 0 gives 0 (lse -inf)."""
-    ctx = _elsewhere(cache, stream)
-    if ctx is not None:
-        with ctx:
+    if stream is not None or _current_device() != cache._index:
+        with _elsewhere(cache, stream):
             return lsa_paged_attn(cache, Q, indices, counts, scale, return_lse, out)
     shape = Q.shape
     _like(cache, Q, "Q", shape)
@@ -827,11 +830,14 @@ def lsa_paged_attn(cache, Q, indices, counts, scale=None, return_lse=False, out=
         out = torch.empty_like(Q)
     else:
         _like(cache, out, "out", shape)
-    lse = torch.empty((B, Nq, Hq), dtype=torch.float32, device=cache.device) if return_lse else None
+    lse = None
+    if return_lse:      # (empty_strided: a microsecond less than empty)
+        lse = torch.empty_strided((B, Nq, Hq), (Nq * Hq, Hq, 1), dtype=torch.float32,
+                                  device=cache.device)
     if Nq > 0:
         _check(_lib.lsa_paged_attn(
             cache._ref, Q.data_ptr(), Nq, Hq, indices.data_ptr(), counts.data_ptr(), s_max,
             1.0 / math.sqrt(d) if scale is None else scale, out.data_ptr(),
             None if lse is None else lse.data_ptr(),
-            torch._C._cuda_getCurrentRawStream(cache._index)))
+            _raw_stream(cache._index)))
     return (out, lse) if return_lse else out

@@ -621,19 +621,32 @@ cudaError_t launch_paged_attn(const lsa_paged_kv& kv, const void* Q, int64_t Nq,
     a.O = (__nv_bfloat16*)O;
     a.lse = lse;
     const int64_t units = kv.B * Nq * kv.Hkv * a.chunks;
-    // CTAs per unit: as many as are resident at once, each with a tile per warp at
-    // least.  16 leave too few places in the GPCs once the grid is over a quarter
-    // of the device (8 sequences of 4 units: 16.7 us with 8, 22.5 us with 16).
+    // CTAs per unit, each with a tile per warp at least.  Up to half of the places
+    // a split shortens the rows' time (4 units of 4,612 keys: 42.3 us with one CTA,
+    // 10.9 with 8, 9.3 with 16), past that only where enough tiles are left to pay
+    // for the merge (128 units of 4,612 keys: 35.0 us with 2, 32.8 with 4; 264 units
+    // of 580 keys: 8.6 us with one, 10.3 with 2), and past one wave never (256 bf16
+    // units: 58.8 us with one, 75.1 with 2).  Clusters of 16 find fewer places in
+    // the GPCs (32 units: 14.6 us with 8, 22.7 with 16, of which 31 fit).
     const int64_t slots = (int64_t)sm_count() * (kv.format == LSA_KV_BF16 && kv.d == 128 ? 3 : 4);
     int c = 1;
-    while (c < PT_MAX_C && units * c * 2 <= (c == 8 ? slots / 4 : slots) &&
-           s_max >= 2 * c * PT_WARPS * 32)
+    while (c < PT_MAX_C) {
+        const int64_t ctas = units * c * 2;
+        const int64_t tiles = s_max / (2 * c * PT_WARPS * 32);     // per warp after the split
+        if (tiles < 1 || ctas > (c == 8 ? slots / 4 : tiles < 6 ? slots / 2 : slots)) break;
         c *= 2;
+    }
     auto run = [&](auto kern, int bytes) {
         cudaError_t e = ensure_smem_attr((const void*)kern, bytes);
-        if (e == cudaSuccess && c > 8)
-            e = cudaFuncSetAttribute((const void*)kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
+        if (c == 1) {
+            kern<<<(unsigned)units, PT_THREADS, bytes, st>>>(kv, a);
+            return cudaGetLastError();
+        }
+        if (c > 8) {
+            e = cudaFuncSetAttribute((const void*)kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            if (e != cudaSuccess) return e;
+        }
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(units * c));
         cfg.blockDim = dim3(PT_THREADS);
