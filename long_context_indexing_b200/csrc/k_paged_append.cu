@@ -17,33 +17,49 @@
 //   * the queries go over (token, head) items, the token fixed for a group of
 //     lanes, so that its cosines stay in registers over the heads; a block of
 //     few new tokens (decode) spreads its heads over all groups instead.
-// Positions are turned in double: t * inv_freq / 2 pi as a product with its
-// rounding error kept, so that far positions lose nothing, reduced to an
-// eighth of a turn before the fp32 sine and cosine.
+// Positions are turned in 64-bit fixed point, so that far positions lose nothing,
+// reduced to an eighth of a turn before the fp32 series.
 #include "paged.cuh"
+#include "ptx.cuh"
 
 namespace lsa {
 
 constexpr int PA_THREADS = 256;
 constexpr int PA_WARPS = PA_THREADS / 32;
 
-// cos and sin of 2 pi * (t * f / (2 pi)).
-__device__ __forceinline__ void turn(int64_t t, float f, float* c, float* s)
+// f / (2 pi) turns per position as a 64-bit fraction of a turn: a position's turn
+// is then a product modulo 2^64, exact but for f's own rounding (2^-63, so 2^-32
+// of a turn at the last position).
+__device__ __forceinline__ uint64_t turns_of(float f)
 {
     constexpr double INV = 0.15915494309189535, INV_LO = -9.839338337591243e-18;   // 1 / (2 pi)
-    const double fd = (double)f, td = (double)t;
+    const double fd = (double)f;
     const double p = fd * INV;
     const double pl = fma(fd, INV, -p) + fd * INV_LO;
-    const double w = td * p;
-    const double wl = fma(td, p, -w) + td * pl;
-    const double r = (w - rint(w)) + wl;             // turns, about [-1/2, 1/2]
-    const double q = rint(4.0 * r);
-    float sn, cs;
-    sincospif((float)(2.0 * (r - 0.25 * q)), &sn, &cs);
-    const int k = (int)q;
-    const float a = (k & 1) ? sn : cs, b = (k & 1) ? cs : sn;
-    *c = ((k + 1) & 2) ? -a : a;
-    *s = (k & 2) ? -b : b;
+    return (uint64_t)__double2ll_rn((p - rint(p)) * 18446744073709551616.0) +
+           (uint64_t)__double2ll_rn(pl * 18446744073709551616.0);
+}
+
+// cos and sin of position t's angle: the nearest quarter turn, and the Taylor
+// series of the rest, |x| <= pi / 4 (sine to x^9, cosine to x^10: 2e-9 and less).
+__device__ __forceinline__ void turn(uint32_t t, uint64_t f, float* c, float* s)
+{
+    const uint64_t a = f * t;
+    const uint32_t k = (uint32_t)((a + (1ull << 61)) >> 62);
+    const float x = (float)(int32_t)((uint32_t)(a >> 32) - (k << 30)) * 1.46291807926715968e-9f;
+    const float y = x * x;                               // (2 pi / 2^32 above)
+    float sn = fmaf(y, 2.75573192e-6f, -1.98412698e-4f);
+    sn = fmaf(y, sn, 8.33333333e-3f);
+    sn = fmaf(y, sn, -1.66666667e-1f);
+    sn = fmaf(x * y, sn, x);
+    float cs = fmaf(y, -2.75573192e-7f, 2.48015873e-5f);
+    cs = fmaf(y, cs, -1.38888889e-3f);
+    cs = fmaf(y, cs, 4.16666667e-2f);
+    cs = fmaf(y, cs, -0.5f);
+    cs = fmaf(y, cs, 1.f);
+    const float u = (k & 1) ? sn : cs, v = (k & 1) ? cs : sn;
+    *c = ((k + 1) & 2) ? -u : u;
+    *s = (k & 2) ? -v : v;
 }
 
 __device__ __forceinline__ void unpack8(float* x, const uint4& w)
@@ -112,7 +128,10 @@ __global__ void __launch_bounds__(PA_THREADS, 3) paged_append_kernel(lsa_paged_k
     constexpr int NP = SCALE_BLOCK / TPW;    // passes over the block's tokens
     constexpr int GROUPS = PA_THREADS / LPT;
     constexpr int QB = 4;                    // query heads in flight per group
-    __shared__ __align__(16) float cos_s[SCALE_BLOCK][D / 2], sin_s[SCALE_BLOCK][D / 2];
+    // (rows 64 bytes apart modulo 128 where two tokens' reads meet)
+    constexpr int TURN_ROW = D / 2 + (D == 64 ? 16 : 0);
+    __shared__ __align__(16) float cos_s[SCALE_BLOCK][TURN_ROW], sin_s[SCALE_BLOCK][TURN_ROW];
+    __shared__ uint4 raw_s[PA_WARPS][QB][2][32];         // what a lane reads, NP or QB pairs
     const int64_t b = blockIdx.y;
     const int64_t start = a.start[b];
     int64_t n = a.n_new ? a.n_new[b] : a.Nq;
@@ -138,17 +157,8 @@ __global__ void __launch_bounds__(PA_THREADS, 3) paged_append_kernel(lsa_paged_k
     }
     if (pg < 0 && threadIdx.x == 0) dev_error(kv.status, DEV_BAD_PAGE, (uint32_t)p0);
 
-    // frequency f of a token at place pos(f): a lane's four or eight turns are
-    // 16-byte runs, the runs of consecutive lanes side by side
     const int nf = a.rot / 2;
     const bool inter = a.interleaved != 0;
-    for (int x = threadIdx.x; x < (i1 - i0) * nf; x += PA_THREADS) {
-        const int i = i0 + x / nf, f = x % nf;
-        const int at = inter ? f : ((f >> 2) & 1) * (nf / 2) + (f >> 3) * 4 + (f & 3);
-        turn(p0 + i, a.inv_freq[f], &cos_s[i][at], &sin_s[i][at]);
-    }
-    __syncthreads();
-
     // a lane's chunks: of the r chunks that turn, (j, j + r/2); of the others
     // likewise
     const int j = lane % LPT;
@@ -156,6 +166,41 @@ __global__ void __launch_bounds__(PA_THREADS, 3) paged_append_kernel(lsa_paged_k
     const bool turns = j < rh;
     const int ca = 8 * (turns ? j : j + rh);
     const int cb = ca + (turns ? 8 * rh : D / 2 - 8 * rh);
+    // ---- a KV head's keys or values of the block, each lane's own chunks; the
+    // first of a warp is on its way while positions are turned ----
+    constexpr int KB = QB / NP;                          // items that raw_s holds
+    auto ask = [&](int it, int at) {
+        const bool is_v = it >= Hkv;
+        const __nv_bfloat16* src = (is_v ? a.v : a.k) + (is_v ? it - Hkv : it) * D;
+        const int64_t stride = is_v ? a.v_stride : a.k_stride;
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+            const int i = p * TPW + lane / LPT;
+            if (i >= i0 && i < i1) {
+                const __nv_bfloat16* r = src + (row0 + i) * stride;
+                ptx::cp_async16(&raw_s[warp][at + p][0][lane], r + ca);
+                ptx::cp_async16(&raw_s[warp][at + p][1][lane], r + cb);
+            }
+        }
+        ptx::cp_async_commit();
+    };
+    if (warp < 2 * Hkv) ask(warp, 0);
+
+    // frequency f of a token at place pos(f): a lane's four or eight turns are
+    // 16-byte runs, the runs of consecutive lanes side by side
+    {
+        int fp = 8;                                      // frequencies, a power of two
+        while (fp < nf) fp *= 2;
+        const int f = threadIdx.x & (fp - 1);
+        if (f < nf) {
+            const uint64_t per = turns_of(a.inv_freq[f]);
+            const int at = inter ? f : ((f >> 2) & 1) * (nf / 2) + (f >> 3) * 4 + (f & 3);
+            for (int i = i0 + threadIdx.x / fp; i < i1; i += PA_THREADS / fp)
+                turn((uint32_t)(p0 + i), per, &cos_s[i][at], &sin_s[i][at]);
+        }
+    }
+    __syncthreads();
+
     auto load_turns = [&](Turns& r, int i) {
         const int at = inter ? 4 * (j + rh) : nf / 2 + 4 * j;
         *reinterpret_cast<float4*>(r.c) = *reinterpret_cast<const float4*>(&cos_s[i][4 * j]);
@@ -166,59 +211,87 @@ __global__ void __launch_bounds__(PA_THREADS, 3) paged_append_kernel(lsa_paged_k
 
     // ---- keys and values ----
     const int64_t slot0 = (int64_t)pg * kv.page + (p0 & (kv.page - 1));
+    int at = 0;
     for (int it = warp; it < 2 * Hkv && pg >= 0; it += PA_WARPS) {
         const bool is_v = it >= Hkv;
         const int h = is_v ? it - Hkv : it;
-        const __nv_bfloat16* src = (is_v ? a.v : a.k) + h * D;
-        const int64_t stride = is_v ? a.v_stride : a.k_stride;
-        uint4 wa[NP], wb[NP];
-#pragma unroll
-        for (int p = 0; p < NP; ++p) {
-            const int i = p * TPW + lane / LPT;
-            wa[p] = wb[p] = make_uint4(0u, 0u, 0u, 0u);
-            if (i >= i0 && i < i1) {
-                const __nv_bfloat16* r = src + (row0 + i) * stride;
-                wa[p] = __ldcs(reinterpret_cast<const uint4*>(r + ca));
-                wb[p] = __ldcs(reinterpret_cast<const uint4*>(r + cb));
-            }
+        const int here = at;
+        if (KB == 2) {                                   // the next item beside this one
+            at = NP - at;
+            if (it + PA_WARPS < 2 * Hkv) ask(it + PA_WARPS, at);
+            else ptx::cp_async_commit();
+            ptx::cp_async_wait<1>();
+        } else {
+            if (it != warp) ask(it, 0);
+            ptx::cp_async_wait<0>();
         }
+        // slot i's values of this lane, rotated
+        auto values = [&](int p, int i, float* lo, float* hi) {
+            unpack8(lo, raw_s[warp][here + p][0][lane]);
+            unpack8(hi, raw_s[warp][here + p][1][lane]);
+            if (!is_v && turns) {
+                Turns r;
+                load_turns(r, i);
+                rotate16(lo, hi, r, inter);
+            }
+        };
         if (!E4M3) {
             __nv_bfloat16* pool = (__nv_bfloat16*)(is_v ? kv.V : kv.K) + h * D;
 #pragma unroll
             for (int p = 0; p < NP; ++p) {
                 const int i = p * TPW + lane / LPT;
                 if (i < i0 || i >= i1) continue;
-                if (!is_v && turns) {
-                    float lo[8], hi[8];
-                    Turns r;
-                    load_turns(r, i);
-                    unpack8(lo, wa[p]);
-                    unpack8(hi, wb[p]);
-                    rotate16(lo, hi, r, inter);
-                    wa[p] = pack8(lo);
-                    wb[p] = pack8(hi);
-                }
+                float lo[8], hi[8];
+                values(p, i, lo, hi);
                 __nv_bfloat16* dst = pool + (slot0 + i) * Hkv * D;
-                *reinterpret_cast<uint4*>(dst + ca) = wa[p];
-                *reinterpret_cast<uint4*>(dst + cb) = wb[p];
+                *reinterpret_cast<uint4*>(dst + ca) = pack8(lo);
+                *reinterpret_cast<uint4*>(dst + cb) = pack8(hi);
             }
             continue;
         }
-        float lo[NP][8], hi[NP][8];
+        // (keys are turned twice, for the maximum and for the codes: held, they would
+        // cost half of the resident CTAs)
         float amax = 0.f;
+        if (is_v) {
+            __nv_bfloat162 m = __floats2bfloat162_rn(0.f, 0.f);   // (passes NaN over)
 #pragma unroll
-        for (int p = 0; p < NP; ++p) {
-            const int i = p * TPW + lane / LPT;
-            unpack8(lo[p], wa[p]);
-            unpack8(hi[p], wb[p]);
-            if (!is_v && turns && i >= i0 && i < i1) {
-                Turns r;
-                load_turns(r, i);
-                rotate16(lo[p], hi[p], r, inter);
+            for (int p = 0; p < NP; ++p) {
+                const int i = p * TPW + lane / LPT;
+                if (i < i0 || i >= i1) continue;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const uint4 w = raw_s[warp][here + p][u][lane];
+                    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        m = __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&x[e])));
+                }
             }
+            amax = fmaxf(__low2float(m), __high2float(m));
+        } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                amax = fmaxf(amax, fmaxf(finite_abs(lo[p][e]), finite_abs(hi[p][e])));
+            for (int p = 0; p < NP; ++p) {
+                const int i = p * TPW + lane / LPT;
+                if (i < i0 || i >= i1) continue;
+                float x[2][8];
+                values(p, i, x[0], x[1]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    amax = fmaxf(amax, fmaxf(fabsf(x[0][e]), fabsf(x[1][e])));
+            }
+        }
+        if (__any_sync(0xffffffffu, isinf(amax))) {      // the largest finite one instead
+            amax = 0.f;
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+                const int i = p * TPW + lane / LPT;
+                if (i < i0 || i >= i1) continue;
+                float lo[8], hi[8];
+                values(p, i, lo, hi);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    amax = fmaxf(amax, fmaxf(finite_abs(lo[e]), finite_abs(hi[e])));
+            }
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
@@ -252,14 +325,17 @@ __global__ void __launch_bounds__(PA_THREADS, 3) paged_append_kernel(lsa_paged_k
             const int i = p * TPW + lane / LPT;
             if (i < i0 || i >= i1) continue;
             uint8_t* dst = pool + (slot0 + i) * Hkv * D;
-            *reinterpret_cast<uint2*>(dst + ca) = codes8(lo[p], inv);
-            *reinterpret_cast<uint2*>(dst + cb) = codes8(hi[p], inv);
+            float x[2][8];
+            values(p, i, x[0], x[1]);
+            *reinterpret_cast<uint2*>(dst + ca) = codes8(x[0], inv);
+            *reinterpret_cast<uint2*>(dst + cb) = codes8(x[1], inv);
         }
         __syncwarp();                        // every lane has read the old scale
         if (lane == 0) *scale = s;
     }
 
     // ---- queries: groups over (token, head), the token fixed ----
+    ptx::cp_async_wait<0>();
     if (a.Hq == 0) return;
     int tp = 1;                              // token slots, a power of two
     while (tp < i1 - i0) tp *= 2;
@@ -271,32 +347,30 @@ __global__ void __launch_bounds__(PA_THREADS, 3) paged_append_kernel(lsa_paged_k
     if (turns) load_turns(r, i);
     const __nv_bfloat16* src = a.q + (row0 + i) * a.q_stride;
     __nv_bfloat16* dst = a.q_out + (row0 + i) * (int64_t)a.Hq * D;
-    for (int h0 = grp / tp; h0 < a.Hq; h0 += QB * hs) {
-        uint4 wa[QB], wb[QB];
-#pragma unroll
-        for (int u = 0; u < QB; ++u) {
-            const int h = h0 + u * hs;
-            if (h < a.Hq) {
-                wa[u] = __ldcs(reinterpret_cast<const uint4*>(src + h * D + ca));
-                wb[u] = __ldcs(reinterpret_cast<const uint4*>(src + h * D + cb));
-            }
+    auto ask_head = [&](int u, int h) {
+        if (h < a.Hq) {
+            ptx::cp_async16(&raw_s[warp][u][0][lane], src + h * D + ca);
+            ptx::cp_async16(&raw_s[warp][u][1][lane], src + h * D + cb);
         }
+        ptx::cp_async_commit();
+    };
+    int h = grp / tp;
 #pragma unroll
-        for (int u = 0; u < QB; ++u) {
-            const int h = h0 + u * hs;
-            if (h < a.Hq) {
-                if (turns) {
-                    float lo[8], hi[8];
-                    unpack8(lo, wa[u]);
-                    unpack8(hi, wb[u]);
-                    rotate16(lo, hi, r, inter);
-                    wa[u] = pack8(lo);
-                    wb[u] = pack8(hi);
-                }
-                *reinterpret_cast<uint4*>(dst + h * D + ca) = wa[u];
-                *reinterpret_cast<uint4*>(dst + h * D + cb) = wb[u];
-            }
+    for (int u = 0; u < QB; ++u) ask_head(u, h + u * hs);
+    for (int u = 0; h < a.Hq; h += hs, u = u + 1 < QB ? u + 1 : 0) {
+        ptx::cp_async_wait<QB - 1>();
+        uint4 xa = raw_s[warp][u][0][lane], xb = raw_s[warp][u][1][lane];
+        ask_head(u, h + QB * hs);
+        if (turns) {
+            float lo[8], hi[8];
+            unpack8(lo, xa);
+            unpack8(hi, xb);
+            rotate16(lo, hi, r, inter);
+            xa = pack8(lo);
+            xb = pack8(hi);
         }
+        *reinterpret_cast<uint4*>(dst + h * D + ca) = xa;
+        *reinterpret_cast<uint4*>(dst + h * D + cb) = xb;
     }
 }
 
