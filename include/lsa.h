@@ -631,6 +631,26 @@ lsa_status lsa_paged_attn(const lsa_paged_kv* kv, const void* Q, int64_t Nq, int
                           const int32_t* indices, const int32_t* counts, int s_max, float scale,
                           void* O, float* lse, void* stream);
 
+/* Workspace bytes for lsa_decode_step_paged (0 on bad arguments; depends on the
+ * device's SM count). */
+size_t lsa_decode_paged_workspace_bytes(const lsa_index* idx, const lsa_paged_kv* kv, int Hq,
+                                        lsa_select_params sp);
+
+/* lsa_decode_step with the keys and values in a paged cache (of the index's B
+ * sequences; a bf16 index): step 1 writes new_latent_k to latent_K as there, and
+ * appends new_k, new_v [B][Hkv][d] to the pages at pos[b] as lsa_paged_append
+ * does, rotating new_k and q [B][Hq][d] by inv_freq, rot_dim, interleaved; step 4
+ * is lsa_paged_attn with scale 1/sqrt(d).  The page of pos[b] must be in the page
+ * table.  The selection is left at the start of the workspace as lsa_decode_step
+ * leaves it.  The index's status word reports the index's errors, the cache's
+ * (lsa_paged_check) the pages'.  Graph-capturable. */
+lsa_status lsa_decode_step_paged(lsa_index* idx, const lsa_paged_kv* kv, void* latent_K,
+                                 const void* new_latent_k, const void* new_k, const void* new_v,
+                                 const void* latent_q, const void* q, const int32_t* pos, int Hq,
+                                 lsa_select_params sp, const float* inv_freq, int rot_dim,
+                                 int interleaved, void* workspace, size_t ws_bytes, void* O,
+                                 void* stream);
+
 /* Reads and clears the cache's status word (synchronises `stream`): LSA_OK, or
  * LSA_ERR_INVALID_ARG when a call since the last check met a position or a
  * page out of range. */

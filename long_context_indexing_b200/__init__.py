@@ -25,7 +25,8 @@ __all__ = [
     "lsa_prefill_partial_slots", "lsa_prefill_select", "lsa_prefill_attend",
     "lsa_prefill_chunk_host", "lsa_prefill_chunk_queries", "LsaTree", "set_wait_limit",
     "lsa_decode_workspace_bytes", "lsa_decode_step", "lsa_select_noalloc",
-    "LsaPagedKV", "lsa_paged_append", "lsa_paged_attn", "library_path", "kernel_launches", "F32",
+    "LsaPagedKV", "lsa_paged_append", "lsa_paged_attn", "lsa_decode_paged_workspace_bytes",
+    "lsa_decode_step_paged", "library_path", "kernel_launches", "F32",
     "BF16",
 ]
 
@@ -111,6 +112,9 @@ def _declare(lib):
         "lsa_paged_append": ([P, P, I64, P, I64, P, I64, P, I64, I, P, P, P, I, I, P], I),
         "lsa_paged_attn": ([P, P, I64, I, P, P, I, F, P, P, P], I),
         "lsa_paged_check": ([P, P], I),
+        "lsa_decode_paged_workspace_bytes": ([P, P, I, SelectParams], SZ),
+        "lsa_decode_step_paged": ([P, P, P, P, P, P, P, P, P, I, SelectParams, P, I, I, P, SZ, P,
+                                   P], I),
     }
     for name, (args, res) in sigs.items():
         fn = getattr(lib, name)
@@ -768,6 +772,16 @@ def _like(cache, t, what, shape):
                         % (what, tuple(shape), cache.device))
 
 
+def _rotation(cache, inv_freq):
+    """Rotated elements of a head."""
+    if inv_freq is None:
+        return 0
+    if inv_freq.dtype is not torch.float32 or inv_freq.dim() != 1 or \
+            not inv_freq.is_contiguous() or inv_freq.get_device() != cache._index:
+        raise TypeError("inv_freq must be a contiguous 1-D float32 tensor on %s" % cache.device)
+    return 2 * inv_freq.shape[0]
+
+
 def lsa_paged_append(cache, k, v, start, n_new=None, q=None, q_out=None, inv_freq=None,
                      interleaved=False, stream=None):
     """Appends k, v [B][Nq][Hkv][d] (bfloat16; slices of a fused projection will do) at positions
@@ -784,12 +798,7 @@ def lsa_paged_append(cache, k, v, start, n_new=None, q=None, q_out=None, inv_fre
     _int32(cache, start, "start", (B,))
     if n_new is not None:
         _int32(cache, n_new, "n_new", (B,))
-    rot = 0
-    if inv_freq is not None:
-        if inv_freq.dtype is not torch.float32 or inv_freq.dim() != 1 or \
-                not inv_freq.is_contiguous() or inv_freq.get_device() != cache._index:
-            raise TypeError("inv_freq must be a contiguous 1-D float32 tensor on %s" % cache.device)
-        rot = 2 * inv_freq.shape[0]
+    rot = _rotation(cache, inv_freq)
     qs, Hq = 0, 0
     if q is not None:
         qs, Hq = _rows(cache, q, "q", B, Nq, None), q.shape[2]
@@ -841,3 +850,54 @@ def lsa_paged_attn(cache, Q, indices, counts, scale=None, return_lse=False, out=
             None if lse is None else lse.data_ptr(),
             _raw_stream(cache._index)))
     return (out, lse) if return_lse else out
+
+
+def lsa_decode_paged_workspace_bytes(index, cache, Hq, budget, window, sinks):
+    """Workspace bytes lsa_decode_step_paged needs."""
+    n = int(_lib.lsa_decode_paged_workspace_bytes(index.handle, cache._ref, int(Hq),
+                                                  SelectParams(budget, window, sinks)))
+    if n == 0:
+        raise LsaError(1, _lib.lsa_last_error().decode())
+    return n
+
+
+def lsa_decode_step_paged(index, cache, latent_K, new_latent_k, new_k, new_v, latent_q, q, pos,
+                          budget, window, sinks, inv_freq=None, interleaved=False, workspace=None,
+                          out=None, stream=None):
+    """One decode step for every sequence over a paged cache (C: lsa_decode_step_paged): the new
+    token's latent key goes to latent_K [B][T_cap][64] and the index, its key (rotated) and value
+    [B][Hkv][d] to the pages at pos[b], and q [B][Hq][d] (rotated) attends over the selection of
+    latent_q [B][64]; returns O [B][Hq][d].  decode_selection_views(workspace, ...) reads the
+    selection."""
+    if stream is not None or _current_device() != cache._index:
+        with _elsewhere(cache, stream):
+            return lsa_decode_step_paged(index, cache, latent_K, new_latent_k, new_k, new_v,
+                                         latent_q, q, pos, budget, window, sinks, inv_freq,
+                                         interleaved, workspace, out)
+    B, Hkv, d = cache.B, cache.Hkv, cache.d
+    Hq = q.shape[1]
+    _like(cache, latent_K, "latent_K", (index.B, index.T_cap, 64))
+    for t, what, shape in ((new_latent_k, "new_latent_k", (B, 64)), (latent_q, "latent_q", (B, 64)),
+                           (new_k, "new_k", (B, Hkv, d)), (new_v, "new_v", (B, Hkv, d)),
+                           (q, "q", (B, Hq, d))):
+        _like(cache, t, what, shape)
+    _int32(cache, pos, "pos", (B,))
+    rot = _rotation(cache, inv_freq)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _like(cache, out, "out", q.shape)
+    if workspace is None:
+        workspace = torch.empty(
+            lsa_decode_paged_workspace_bytes(index, cache, Hq, budget, window, sinks),
+            dtype=torch.uint8, device=cache.device)
+    elif workspace.get_device() != cache._index or not workspace.is_contiguous() or \
+            workspace.dtype is not torch.uint8:
+        raise TypeError("workspace must be a contiguous uint8 tensor on %s" % cache.device)
+    _check(_lib.lsa_decode_step_paged(
+        index.handle, cache._ref, latent_K.data_ptr(), new_latent_k.data_ptr(), new_k.data_ptr(),
+        new_v.data_ptr(), latent_q.data_ptr(), q.data_ptr(), pos.data_ptr(), Hq,
+        SelectParams(budget, window, sinks), None if inv_freq is None else inv_freq.data_ptr(),
+        rot, bool(interleaved), workspace.data_ptr(), workspace.numel(), out.data_ptr(),
+        _raw_stream(cache._index)))
+    return out

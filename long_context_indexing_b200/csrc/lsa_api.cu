@@ -1392,6 +1392,117 @@ lsa_status lsa_paged_attn(const lsa_paged_kv* kv, const void* Q, int64_t Nq, int
     return LSA_OK;
 }
 
+// Decode workspace over a paged cache: the selection part of decode_layout (with
+// a head shape that makes its attention part small), then the rotated queries.
+namespace {
+struct PagedDecodeLayout {
+    DecodeLayout sel;
+    size_t q, total;
+};
+PagedDecodeLayout paged_decode_layout(const lsa_index* idx, const lsa_paged_kv* kv, int Hq,
+                                      lsa_select_params sp)
+{
+    PagedDecodeLayout L;
+    L.sel = decode_layout(idx, 1, 1, 64, sp);
+    L.q = L.sel.total;
+    L.total = L.q + al256((size_t)kv->B * Hq * kv->d * 2);
+    return L;
+}
+}  // namespace
+
+size_t lsa_decode_paged_workspace_bytes(const lsa_index* idx, const lsa_paged_kv* kv, int Hq,
+                                        lsa_select_params sp)
+{
+    if (!idx || sp.budget < 0 || sp.window < 0 || sp.sinks < 0 || check_paged(kv) != LSA_OK ||
+        check_paged_heads(kv, Hq) != LSA_OK)
+        return 0;
+    return paged_decode_layout(idx, kv, Hq, sp).total;
+}
+
+lsa_status lsa_decode_step_paged(lsa_index* idx, const lsa_paged_kv* kv, void* latent_K,
+                                 const void* new_latent_k, const void* new_k, const void* new_v,
+                                 const void* latent_q, const void* q, const int32_t* pos, int Hq,
+                                 lsa_select_params sp, const float* inv_freq, int rot_dim,
+                                 int interleaved, void* workspace, size_t ws_bytes, void* O,
+                                 void* stream)
+{
+    NvtxRange nv("lsa_decode_step_paged");
+    if (!idx || !latent_K || !new_latent_k || !new_k || !new_v || !latent_q || !q || !pos ||
+        !workspace || !O)
+        return fail(LSA_ERR_INVALID_ARG, "NULL argument");
+    lsa_status s = check_paged(kv);
+    if (s == LSA_OK) s = check_paged_heads(kv, Hq);
+    if (s == LSA_OK) s = check_rotation(kv, inv_freq, rot_dim);
+    if (s != LSA_OK) return s;
+    const IndexView& v = idx->v;
+    if (v.dtype != LSA_BF16) return fail(LSA_ERR_UNSUPPORTED, "a paged cache needs a bf16 index");
+    if (v.B != kv->B)
+        return fail(LSA_ERR_INVALID_ARG, "the index holds %lld sequences, the cache %lld",
+                    (long long)v.B, (long long)kv->B);
+    const int s_max = sp.budget + sp.window + sp.sinks;
+    s = check_select(idx, sp, s_max);
+    if (s != LSA_OK) return s;
+    const void* ptrs[] = {latent_K, new_latent_k, new_k, new_v, latent_q, q, pos, workspace, O};
+    for (const void* p : ptrs)
+        if (!aligned16(p)) return fail(LSA_ERR_ALIGNMENT, "device pointers must be 16-byte aligned");
+    if (idx->n_blk < 1 || idx->n_blk * v.G >= v.NP)
+        return fail(LSA_ERR_INVALID_ARG,
+                    "decode needs at least one closed block and room for an open block");
+    const PagedDecodeLayout L = paged_decode_layout(idx, kv, Hq, sp);
+    if (ws_bytes < L.total)
+        return fail(LSA_ERR_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, L.total);
+    cudaStream_t st = (cudaStream_t)stream;
+    char* base = (char*)workspace;
+    int32_t* indices = (int32_t*)(base + L.sel.indices);
+    int32_t* counts = (int32_t*)(base + L.sel.counts);
+    SelectWs w = select_ws_carve(base + L.sel.sel, v, 1);
+    w.dl_s = (float*)(base + L.sel.dl_s);
+    w.dl_g = (int32_t*)(base + L.sel.dl_g);
+    w.dl_n = (int32_t*)(base + L.sel.dl_n);
+    w.dl_tau = (float*)(base + L.sel.dl_tau);
+    w.n_slice = L.sel.n_slice;
+    double* app_score = (double*)(base + L.sel.app_score);
+    int32_t* app_g = (int32_t*)(base + L.sel.app_g);
+    int32_t* app_slot = (int32_t*)(base + L.sel.app_slot);
+    w.app_score = app_score;
+    w.app_g = app_g;
+    w.app_slot = app_slot;
+    w.app_n = L.sel.n_slice;
+    if (!idx->status_clean) {
+        cudaError_t e = cudaMemsetAsync(v.status, 0, 8 * sizeof(uint32_t), st);
+        if (e != cudaSuccess) return cuda_fail(e, "status clear");
+        idx->status_clean = true;
+    }
+    s = dbg_index(v, idx->n_blk, st, "index before decode step");
+    if (s != LSA_OK) return s;
+    // latent row and scores (no contiguous K and V rows: 0 heads), then the pages
+    cudaError_t e = launch_decode_prep(v, idx->n_blk, latent_K, nullptr, nullptr, new_latent_k,
+                                       nullptr, nullptr, latent_q, pos, 0, 0, sp.window, w,
+                                       app_score, app_g, app_slot, L.sel.n_slice, nullptr, 0, st);
+    if (e != cudaSuccess) return cuda_fail(e, "decode append/nominate");
+    AppendArgs a{};
+    a.k = (const __nv_bfloat16*)new_k;
+    a.v = (const __nv_bfloat16*)new_v;
+    a.q = (const __nv_bfloat16*)q;
+    a.q_out = (__nv_bfloat16*)(base + L.q);
+    a.k_stride = a.v_stride = (int64_t)kv->Hkv * kv->d;
+    a.q_stride = (int64_t)Hq * kv->d;
+    a.Nq = 1;
+    a.Hq = Hq;
+    a.start = pos;
+    a.inv_freq = inv_freq;
+    a.rot = rot_dim;
+    a.interleaved = interleaved != 0;
+    e = launch_paged_append(*kv, a, st);
+    if (e != cudaSuccess) return cuda_fail(e, "paged append");
+    e = launch_decode_finish(v, idx->n_blk, latent_q, pos, sp, indices, counts, s_max, w, st);
+    if (e != cudaSuccess) return cuda_fail(e, "decode select");
+    e = launch_paged_attn(*kv, base + L.q, 1, Hq, indices, counts, s_max,
+                          (float)(1.0 / sqrt((double)kv->d)), O, nullptr, st);
+    if (e != cudaSuccess) return cuda_fail(e, "paged attention");
+    return LSA_OK;
+}
+
 lsa_status lsa_paged_check(const lsa_paged_kv* kv, void* stream)
 {
     lsa_status s = check_paged(kv);

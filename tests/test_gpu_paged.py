@@ -546,3 +546,117 @@ def test_wrong_tensors_are_refused():
     assert lsa.lsa_paged_attn(c, Q[:, :0].contiguous(), idx[:, :0].contiguous(),
                               cnt[:, :0].contiguous()).shape == (2, 0, 4, 64)
     assert lsa.kernel_launches() == n0
+
+
+@pytest.mark.parametrize("dtype,Hq,Hkv,d", [(torch.bfloat16, 32, 4, 128), (FP8, 12, 4, 64),
+                                            (FP8, 32, 4, 128)])
+def test_decode_steps_over_pages(dtype, Hq, Hkv, d):
+    # every step: the selection is lsa_decode_step's over the same latents; the appended
+    # token and the attention over the selection are those of binary64
+    import synth
+    w = synth.workload("decode", T=4096, B=3, M=64, G=64, k=4, L=3, R=600, W=8, S=4, steps=20,
+                       Hq=Hq, Hkv=Hkv, d=d, dtype="bf16")
+    inp = synth.decode_inputs(w, 13, "cpu")
+    page, t_cap = 32, w.T + 20 + w.p * w.G
+    rng = np.random.default_rng(7)
+    n_pages = w.B * ((t_cap + page - 1) // page)
+    c = lsa.LsaPagedKV.empty(w.B, n_pages + 1, page, n_pages // w.B, Hkv, d, dtype)
+    c.page_table.copy_(torch.from_numpy(rng.permutation(n_pages).reshape(w.B, -1).astype(np.int32)))
+    inv = _freq(d)
+    dinv = torch.from_numpy(inv).cuda()
+    lat = torch.zeros(w.B, t_cap, 64, dtype=torch.bfloat16, device="cuda")
+    lat[:, :w.T] = inp["latent_K"][:, :w.T].cuda()
+    lsa.lsa_paged_append(c, inp["K"][:, :w.T].cuda(), inp["V"][:, :w.T].cuda(),
+                         torch.zeros(w.B, dtype=torch.int32, device="cuda"), inv_freq=dinv)
+    idx = lsa.LsaIndex(w.B, t_cap, w.p, w.G, w.k, w.L, lsa.BF16)
+    idx.build(lat, w.T)
+    # the contiguous path beside it, for the selections
+    lat2 = lat.clone()
+    idx2 = lsa.LsaIndex(w.B, t_cap, w.p, w.G, w.k, w.L, lsa.BF16)
+    idx2.build(lat2, w.T)
+    heads = (8, 4) if Hq == 12 else (Hq, Hkv)
+    K2 = torch.zeros(w.B, t_cap, heads[1], d, dtype=torch.bfloat16, device="cuda")
+    V2 = torch.zeros_like(K2)
+    ws = torch.empty(lsa.lsa_decode_paged_workspace_bytes(idx, c, Hq, w.R, w.W, w.S),
+                     dtype=torch.uint8, device="cuda")
+    ws2 = torch.empty(lsa.lsa_decode_workspace_bytes(idx2, *heads, d, w.R, w.W, w.S),
+                      dtype=torch.uint8, device="cuda")
+    for t in range(12):
+        pos = torch.full((w.B,), w.T + t, dtype=torch.int32, device="cuda")
+        new = [inp[n][t].contiguous().cuda() for n in ("new_latent_k", "new_k", "new_v", "latent_q", "q")]
+        before = _state(c)
+        O = lsa.lsa_decode_step_paged(idx, c, lat, *new, pos, w.R, w.W, w.S, inv_freq=dinv,
+                                      workspace=ws)
+        sel, cnt = lsa.decode_selection_views(ws, w.B, w.s_max)
+        lsa.lsa_decode_step(idx2, lat2, K2, V2, new[0], new[1][:, :heads[1]].contiguous(),
+                            new[2][:, :heads[1]].contiguous(), new[3],
+                            new[4][:, :heads[0]].contiguous(), pos, w.R, w.W, w.S, workspace=ws2)
+        sel2, cnt2 = lsa.decode_selection_views(ws2, w.B, w.s_max)
+        assert torch.equal(cnt, cnt2) and torch.equal(sel, sel2) and torch.equal(lat, lat2)
+        k, v, q = (new[i].cpu()[:, None] for i in (1, 2, 4))
+        _check_append(c, before, (k, v, pos.cpu().numpy(), [1] * w.B, inv, False, None))
+        # the queries as the step rotates them
+        qr = torch.empty_like(q.cuda())
+        spare = lsa.LsaPagedKV(c.k_pages.clone(), c.v_pages.clone(), c.page_table,
+                               None if c.scales is None else c.scales.clone())
+        lsa.lsa_paged_append(spare, k.cuda(), v.cuda(), pos, q=q.cuda(), q_out=qr, inv_freq=dinv)
+        O2, lse = lsa.lsa_paged_attn(c, qr, sel[:, None].contiguous(), cnt[:, None].contiguous(),
+                                     return_lse=True)
+        assert torch.equal(O, O2[:, 0])
+        _check_attn(c, qr, sel[:, None].cpu().numpy(), cnt[:, None].cpu().numpy(), 1 / np.sqrt(d),
+                    O[:, None], lse)
+    idx.check()
+    c.check()
+
+
+def test_decode_step_captured_and_replayed():
+    # one captured step replayed with the position and the inputs changed in place gives
+    # what eager steps give
+    import synth
+    w = synth.workload("decode", T=2048, B=2, M=32, G=64, k=4, L=3, R=300, W=16, S=4, steps=8,
+                       Hq=8, Hkv=2, d=64, dtype="bf16")
+    inp = synth.decode_inputs(w, 17, "cpu")
+    page, t_cap = 16, w.T + 8 + w.p * w.G
+    dinv = torch.from_numpy(_freq(64)).cuda()
+
+    def setup():
+        mp = (t_cap + page - 1) // page
+        c = lsa.LsaPagedKV.empty(w.B, w.B * mp, page, mp, w.Hkv, w.d, FP8)
+        c.page_table.copy_(torch.arange(w.B * mp, dtype=torch.int32).view(w.B, mp))
+        lat = torch.zeros(w.B, t_cap, 64, dtype=torch.bfloat16, device="cuda")
+        lat[:, :w.T] = inp["latent_K"][:, :w.T].cuda()
+        lsa.lsa_paged_append(c, inp["K"][:, :w.T].cuda(), inp["V"][:, :w.T].cuda(),
+                             torch.zeros(w.B, dtype=torch.int32, device="cuda"), inv_freq=dinv)
+        idx = lsa.LsaIndex(w.B, t_cap, w.p, w.G, w.k, w.L, lsa.BF16)
+        idx.build(lat, w.T)
+        ws = torch.empty(lsa.lsa_decode_paged_workspace_bytes(idx, c, w.Hq, w.R, w.W, w.S),
+                         dtype=torch.uint8, device="cuda")
+        return c, lat, idx, ws
+
+    names = ("new_latent_k", "new_k", "new_v", "latent_q", "q")
+    want = []
+    c, lat, idx, ws = setup()
+    for t in range(6):
+        pos = torch.full((w.B,), w.T + t, dtype=torch.int32, device="cuda")
+        want.append(lsa.lsa_decode_step_paged(idx, c, lat, *[inp[n][t].contiguous().cuda() for n in names],
+                                              pos, w.R, w.W, w.S, inv_freq=dinv, workspace=ws).clone())
+    c, lat, idx, ws = setup()
+    x = [inp[n][0].contiguous().cuda() for n in names]
+    pos = torch.full((w.B,), w.T, dtype=torch.int32, device="cuda")
+    out = torch.empty_like(x[4])
+    # one eager step first: the same token again, so that the capture finds the index ready
+    lsa.lsa_decode_step_paged(idx, c, lat, *x, pos, w.R, w.W, w.S, inv_freq=dinv, workspace=ws, out=out)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        lsa.lsa_decode_step_paged(idx, c, lat, *x, pos, w.R, w.W, w.S, inv_freq=dinv, workspace=ws,
+                                  out=out)
+    for t in range(6):
+        for a, n in zip(x, names):
+            a.copy_(inp[n][t])
+        pos.fill_(w.T + t)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[t]), t
+    c.check()
+    idx.check()

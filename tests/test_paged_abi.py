@@ -82,6 +82,42 @@ def test_empty_calls_and_calls_without_gpu():
     assert lsa._lib.lsa_paged_check(ctypes.byref(_kv()), None) == 4
 
 
+def _index(B=2, dtype=lsa.BF16, T_cap=8192):
+    P = lsa.IndexParams(4, 256, 8, 3)
+    need = lsa._lib.lsa_index_bytes(B, T_cap, P, dtype)
+    h = ctypes.c_void_p()
+    assert lsa._lib.lsa_index_init(ctypes.c_void_p(FAKE), need, B, T_cap, P, dtype,
+                                   ctypes.byref(h)) == 0
+    return h
+
+
+def _step(h, kv=None, **over):
+    S = over.pop("sp", lsa.SelectParams(256, 64, 4))
+    a = dict(lat=FAKE, nlk=FAKE, nk=FAKE, nv=FAKE, lq=FAKE, q=FAKE, pos=FAKE, Hq=8, sp=S, inv=FAKE,
+             rot=128, inter=0, ws=FAKE, bytes=1 << 40, O=FAKE, stream=None)
+    a.update(over)
+    return lsa._lib.lsa_decode_step_paged(h, ctypes.byref(kv or _kv()), *a.values())
+
+
+def test_decode_step_arguments_refused():
+    h = _index()
+    for over, code in ((dict(lat=None), 1), (dict(nk=None), 1), (dict(q=None), 1), (dict(O=None), 1),
+                       (dict(ws=None), 1), (dict(Hq=7), 1), (dict(inv=None), 1), (dict(rot=24), 1),
+                       (dict(nv=FAKE + 8), 2), (dict(sp=lsa.SelectParams(256, 2, 4)), 7)):
+        assert _step(h, **over) == code, over
+    assert _step(h, _kv(B=3)) == 1                          # not the index's sequences
+    assert _step(h, _kv(page=24)) == 7
+    assert _step(h) == 1                                    # no closed block yet
+    assert _step(_index(dtype=lsa.F32)) == 7
+    S = lsa.SelectParams(256, 64, 4)
+    f = lsa._lib.lsa_decode_paged_workspace_bytes
+    n = f(h, ctypes.byref(_kv()), 8, S)
+    assert n > 2 * 324 * 4 + 2 * 8 * 128 * 2
+    assert f(h, ctypes.byref(_kv(d=96)), 8, S) == 0 and f(h, ctypes.byref(_kv()), 7, S) == 0
+    assert f(None, ctypes.byref(_kv()), 8, S) == 0
+    assert f(h, ctypes.byref(_kv()), 8, lsa.SelectParams(-1, 64, 4)) == 0
+
+
 def test_handle_wants_cuda_tensors_of_one_kind():
     k = torch.zeros(4, 16, 2, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError):
