@@ -626,7 +626,9 @@ lsa_status lsa_paged_append(const lsa_paged_kv* kv, const void* k, int64_t k_str
  * on a page outside [0, n_pages), is skipped and recorded in the status.  lse
  * (nullable) [B][Nq][Hq] f32: max + ln(sum) of the scaled logits.  For 8-bit
  * pages the scales may be any positive numbers.  Asynchronous on `stream`,
- * graph-capturable, no workspace. */
+ * graph-capturable, no workspace.  Slots that no row lists are never read.  An
+ * infinity or NaN in a listed row, or in Q, makes the results that it enters
+ * non-finite (NaN where exact arithmetic may give an infinity). */
 lsa_status lsa_paged_attn(const lsa_paged_kv* kv, const void* Q, int64_t Nq, int Hq,
                           const int32_t* indices, const int32_t* counts, int s_max, float scale,
                           void* O, float* lse, void* stream);

@@ -89,13 +89,16 @@ def append(state, k, v, start, n_new, inv_freq, inter, q=None):
     return q_out
 
 
-def attend(Kv, Vv, table, Q, idx, cnt, scale):
+def attend(Kv, Vv, table, Q, idx, cnt, scale, sV=None):
     """Values Kv, Vv [n_pages][page][Hkv][d] (codes times scales): per row and head the output,
-    its sum of p |v| (what errors of p scale with), the largest sum of |q k| and lse."""
+    its sum of p |v| (what errors of p scale with), the largest sum of |q k| and lse; with V's
+    scales sV [n_pages][page][Hkv] the second is (that, max p sV * sum |codes|), what an
+    absolute error of every p sV relative to the largest scales with."""
     n_pages, page, Hkv, d = Kv.shape
     B, Nq, Hq, _ = Q.shape
     O, A = np.zeros((B, Nq, Hq, d)), np.zeros((B, Nq, Hq, d))
     Z, L = np.zeros((B, Nq, Hq)), np.full((B, Nq, Hq), -np.inf)
+    F = np.zeros((B, Nq, Hq, d))
     for b in range(B):
         for i in range(Nq):
             t = np.asarray(idx[b, i, :max(0, cnt[b, i])], np.int64)
@@ -115,4 +118,7 @@ def attend(Kv, Vv, table, Q, idx, cnt, scale):
                 p /= p.sum()
                 O[b, i, h], A[b, i, h] = p @ vs, p @ np.abs(vs)
                 Z[b, i, h] = scale * (np.abs(ks) @ np.abs(Q[b, i, h])).max()
-    return O, A, Z, L
+                if sV is not None:
+                    sv = sV[pg, t % page, g]
+                    F[b, i, h] = (p * sv).max() * (np.abs(vs) / sv[:, None]).sum(0)
+    return O, (A if sV is None else (A, F)), Z, L

@@ -10,7 +10,10 @@ fp16 2^-11, e4m3 2^-4 or half its spacing):
   attention    logits in fp32 over d products: dz = 2^-18 of the largest sum of
                |q k|; weights rounded to fp16 at least, 2^-11, and exp, sum and
                rescaling in fp32: (2^-10 + 4 dz) sum p |v|; output 2^-8 |o| in bf16;
-               lse 2 dz + 2^-19 (1 + |lse|).
+               lse 2 dz + 2^-19 (1 + |lse|).  8-bit pages: the largest weight p sV is
+               held at 2^7 or more, so a weight below fp16's normal range is off by
+               half of 2^-24 at most, 2^-32 of the largest: 2^-32 max(p sV) sum |codes|,
+               twice that for its fp32 exponential.
 """
 import numpy as np
 import pytest
@@ -276,11 +279,14 @@ def test_append_rotates_far_positions_and_in_place():
 # ---- attention ----------------------------------------------------------------------------------
 
 def _check_attn(c, Q, idx, cnt, scale, O, lse):
-    Kv, Vv = _values(_state(c))
+    st = _state(c)
+    Kv, Vv = _values(st)
     Qd = Q.float().cpu().double().numpy()
-    ro, ra, rz, rl = plain.attend(Kv, Vv, c.page_table.cpu().numpy(), Qd, idx, cnt, scale)
+    sV = None if st["scales"] is None else np.repeat(st["scales"], plain.BLOCK, axis=1)[:, :, 1]
+    ro, ra, rz, rl = plain.attend(Kv, Vv, c.page_table.cpu().numpy(), Qd, idx, cnt, scale, sV)
+    ra, floor = ra if sV is not None else (ra, 0.0)
     dz = 2.0 ** -18 * rz
-    tol = 2.0 ** -8 * np.abs(ro) + (2.0 ** -10 + 4 * dz)[..., None] * ra + 1e-38
+    tol = 2.0 ** -8 * np.abs(ro) + (2.0 ** -10 + 4 * dz)[..., None] * ra + 2.0 ** -31 * floor + 1e-38
     go = O.float().cpu().double().numpy()
     assert (np.abs(go - ro) <= tol).all(), np.max(np.abs(go - ro) / tol)
     gl = lse.cpu().double().numpy()
