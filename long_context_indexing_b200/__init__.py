@@ -747,21 +747,20 @@ def _int32(cache, t, what, shape):
 def _rows(cache, t, what, B, Nq, H):
     """Elements between consecutive token rows of a bfloat16 [B][Nq][H][d] tensor whose rows
     are contiguous (a slice of a wider projection, for instance); H None: any."""
-    if t.dtype is not _BF16 or t.get_device() != cache._index or t.dim() != 4:
+    shape = t.shape
+    if t.dtype is not _BF16 or t.get_device() != cache._index or len(shape) != 4:
         raise TypeError("%s must be a bfloat16 tensor [B][Nq][heads][d] on %s"
                         % (what, cache.device))
-    b, n, h, d = t.shape
+    b, n, h, d = shape
     if b != B or n != Nq or d != cache.d or (h != H and H is not None):
         raise ValueError("%s has shape %s, not [%d][%d][%s][%d]"
-                         % (what, tuple(t.shape), B, Nq, "heads" if H is None else H, cache.d))
-    if t.is_contiguous():
-        return h * d
+                         % (what, tuple(shape), B, Nq, "heads" if H is None else H, cache.d))
     sb, sn, sh, se = t.stride()
     row = sn if n > 1 else (sb if b > 1 else h * d)
     if se != 1 or (sh != d and h > 1) or (sb != n * row and b > 1 and n > 0):
         raise ValueError("%s must have contiguous rows at one distance (strides %s)"
                          % (what, t.stride()))
-    return row
+    return row if n > 0 else h * d
 
 
 def _like(cache, t, what, shape):
@@ -794,7 +793,9 @@ def lsa_paged_append(cache, k, v, start, n_new=None, q=None, q_out=None, inv_fre
             return lsa_paged_append(cache, k, v, start, n_new, q, q_out, inv_freq, interleaved)
     B, Nq = cache.B, k.shape[1]
     ks = _rows(cache, k, "k", B, Nq, cache.Hkv)
-    vs = _rows(cache, v, "v", B, Nq, cache.Hkv)
+    # (slices of one projection: what held for k holds for v)
+    vs = ks if v.stride() == k.stride() and v.shape == k.shape and v.dtype is _BF16 and \
+        v.get_device() == cache._index else _rows(cache, v, "v", B, Nq, cache.Hkv)
     _int32(cache, start, "start", (B,))
     if n_new is not None:
         _int32(cache, n_new, "n_new", (B,))
