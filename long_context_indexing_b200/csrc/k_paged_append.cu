@@ -28,8 +28,8 @@
 // Measured (B200): 32,768 tokens of 32/4 heads of 128 into 8-bit pages 102 us (637.6
 // MB, 6.25 TB/s, 0.95 of a copy's rate: HBM); 2 x 4,096 tokens of 16/2 heads into
 // bf16 pages 18.3 us (4.6 TB/s; 514 CTAs, a little over one wave of 444); 7 padded
-// prompts of up to 1,021 tokens of 24/8 heads of 64 11.7 us (one wave of latencies:
-// start 1.0 us, turns 1.5, keys and values 3.6, queries 2.8); 8 tokens 4.4 us.
+// prompts of up to 1,021 tokens of 24/8 heads of 64 10.7 us (waves of latencies:
+// start 1.0 us, page and turns 2, keys and values 3.6, queries 2.8); 8 tokens 3.5 us.
 #include "paged.cuh"
 #include "ptx.cuh"
 
@@ -143,13 +143,16 @@ __global__ void __launch_bounds__(PA_THREADS, 3) paged_append_kernel(lsa_paged_k
     constexpr int TURN_ROW = D / 2 + (D == 64 ? 16 : 0);
     __shared__ __align__(16) float cos_s[SCALE_BLOCK][TURN_ROW], sin_s[SCALE_BLOCK][TURN_ROW];
     __shared__ uint4 raw_s[PA_WARPS][QB][2][32];         // what a lane reads, NP or QB pairs
+    // one CTA for a block's keys, values and queries, or one for each part
+    const bool do_kv = blockIdx.z == 0, do_q = a.Hq > 0 && blockIdx.z == gridDim.z - 1;
     const int64_t b = blockIdx.y;
     const int64_t start = a.start[b];
     int64_t n = a.n_new ? a.n_new[b] : a.Nq;
     if (n > a.Nq) n = a.Nq;
     if (n <= 0) return;
     if (start < 0) {
-        if (blockIdx.x == 0 && threadIdx.x == 0) dev_error(kv.status, DEV_BAD_PAGE, (uint32_t)start);
+        if (blockIdx.x == 0 && threadIdx.x == 0 && do_kv)
+            dev_error(kv.status, DEV_BAD_PAGE, (uint32_t)start);
         return;
     }
     const int64_t p0 = (start / SCALE_BLOCK + blockIdx.x) * SCALE_BLOCK;
@@ -166,7 +169,7 @@ __global__ void __launch_bounds__(PA_THREADS, 3) paged_append_kernel(lsa_paged_k
         pg = kv.page_table[b * kv.max_pages + (p0 >> (__ffs(kv.page) - 1))];
         if (pg < 0 || pg >= kv.n_pages) pg = -1;
     }
-    if (pg < 0 && threadIdx.x == 0) dev_error(kv.status, DEV_BAD_PAGE, (uint32_t)p0);
+    if (pg < 0 && threadIdx.x == 0 && do_kv) dev_error(kv.status, DEV_BAD_PAGE, (uint32_t)p0);
 
     const int nf = a.rot / 2;
     const bool inter = a.interleaved != 0;
@@ -195,7 +198,7 @@ __global__ void __launch_bounds__(PA_THREADS, 3) paged_append_kernel(lsa_paged_k
         }
         ptx::cp_async_commit();
     };
-    if (warp < 2 * Hkv) ask(warp, 0);
+    if (do_kv && warp < 2 * Hkv) ask(warp, 0);
 
     // frequency f of a token at place pos(f): a lane's four or eight turns are
     // 16-byte runs, the runs of consecutive lanes side by side
@@ -223,7 +226,7 @@ __global__ void __launch_bounds__(PA_THREADS, 3) paged_append_kernel(lsa_paged_k
     // ---- keys and values ----
     const int64_t slot0 = (int64_t)pg * kv.page + (p0 & (kv.page - 1));
     int at = 0;
-    for (int it = warp; it < 2 * Hkv && pg >= 0; it += PA_WARPS) {
+    for (int it = warp; it < 2 * Hkv && do_kv && pg >= 0; it += PA_WARPS) {
         const bool is_v = it >= Hkv;
         const int h = is_v ? it - Hkv : it;
         const int here = at;
@@ -347,7 +350,7 @@ __global__ void __launch_bounds__(PA_THREADS, 3) paged_append_kernel(lsa_paged_k
 
     // ---- queries: groups over (token, head), the token fixed ----
     ptx::cp_async_wait<0>();
-    if (a.Hq == 0) return;
+    if (!do_q) return;
     int tp = 1;                              // token slots, a power of two
     while (tp < i1 - i0) tp *= 2;
     const int grp = threadIdx.x / LPT;
@@ -388,7 +391,12 @@ __global__ void __launch_bounds__(PA_THREADS, 3) paged_append_kernel(lsa_paged_k
 cudaError_t launch_paged_append(const lsa_paged_kv& kv, const AppendArgs& a, cudaStream_t st)
 {
     // Nq consecutive positions touch at most (Nq + 14) / 16 + 1 blocks
-    const dim3 grid((unsigned)((a.Nq + SCALE_BLOCK - 2) / SCALE_BLOCK + 1), (unsigned)kv.B);
+    const int64_t blocks = (a.Nq + SCALE_BLOCK - 2) / SCALE_BLOCK + 1;
+    // up to two waves the queries get CTAs of their own (8 tokens 4.2 us against 3.5,
+    // 7 padded prompts 11.5 against 10.7); past that the turns computed twice cost more
+    // than the shorter CTAs bring (32,768 tokens 101 us against 107)
+    const bool split = a.Hq > 0 && blocks * kv.B <= 2 * 3 * (int64_t)sm_count();
+    const dim3 grid((unsigned)blocks, (unsigned)kv.B, split ? 2u : 1u);
     auto run = [&](auto kern) { kern<<<grid, PA_THREADS, 0, st>>>(kv, a); };
     if (kv.format == LSA_KV_E4M3)
         kv.d == 64 ? run(paged_append_kernel<true, 64>) : run(paged_append_kernel<true, 128>);
