@@ -83,11 +83,12 @@ struct PagedCfg {
     static constexpr int EPT = PT_H * D / PT_THREADS; // merged elements per thread
     // a warp's positions [2][32], pages [32] and scales [2][2][32] of tiles
     static constexpr int META = 4 * 32 * (E4M3 ? 2 + 1 + 4 : 2 + 1);
-    static constexpr int BYTES = PT_WARPS * (RING + META) + 4 * 3 * PT_WARPS * PT_H;
-    // after the loop: O^T of a warp at its ring, the cluster's slices behind the
-    // first warp's, the CTAs' references and sums in place of the positions
-    static constexpr int RECV = 4 * PT_H * D;
-    static_assert(2 * RECV <= RING && 4 * 3 * PT_H * PT_MAX_C <= PT_WARPS * META, "merge arrays fit");
+    // the slices a CTA of a cluster receives (c slices of ceil(threads / c) threads'
+    // elements) and the CTAs' references and sums
+    static constexpr int RECV = 4 * EPT * (PT_THREADS + PT_MAX_C), RECV_ML = 4 * 3 * PT_H * PT_MAX_C;
+    static constexpr int BYTES =
+        PT_WARPS * (RING + META) + RECV + RECV_ML + 4 * 3 * PT_WARPS * PT_H;
+    static_assert(4 * PT_H * D <= RING, "a warp's O^T takes its ring's place");
 };
 
 struct PagedAttnArgs {
@@ -179,12 +180,15 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
 {
     using C = PagedCfg<E4M3, D>;
     extern __shared__ __align__(128) char smem[];
-    float* recv = reinterpret_cast<float*>(smem + C::RECV);
-    float* recv_ml = reinterpret_cast<float*>(smem + PT_WARPS * C::RING);   // [CTA][m1, m2, l][head]
-    float* ml_s = reinterpret_cast<float*>(smem + PT_WARPS * (C::RING + C::META));   // [warp] likewise
+    char* tail = smem + PT_WARPS * (C::RING + C::META);
+    float* recv = reinterpret_cast<float*>(tail);
+    float* recv_ml = reinterpret_cast<float*>(tail + C::RECV);              // [CTA][m1, m2, l][head]
+    float* ml_s = reinterpret_cast<float*>(tail + C::RECV + C::RECV_ML);    // [warp] likewise
     uint32_t rank, n_cta;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(n_cta));
+    // the CTAs of the cluster have started before any is written to
+    if (n_cta > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r8 = lane >> 2, t4 = lane & 3;
     const int64_t unit = blockIdx.x / n_cta;
@@ -511,7 +515,6 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
     // ---- merge: lanes, warps, CTAs ----
     ptx::cp_async_wait<0>();
     __syncwarp();                                       // the rings are free
-    if (n_cta > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     float* o_s = reinterpret_cast<float*>(smem);        // warp w's O^T at w * RING
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
@@ -558,10 +561,9 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
         for (int i = 0; i < C::EPT; ++i) o[i] += f * src[i * 64];
     }
     if (n_cta > 1) {
-        // every CTA's rings are free
-        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
         // thread t's elements go to CTA t / tpc, place (source CTA, t % tpc)
-        const uint32_t tpc = PT_THREADS / n_cta;
+        const uint32_t tpc = (PT_THREADS + n_cta - 1) / n_cta;
         const uint32_t to = threadIdx.x / tpc, at = threadIdx.x % tpc;
         const uint32_t dst = cluster_addr(recv, to) + 4 * C::EPT * (rank * tpc + at);
 #pragma unroll
@@ -589,8 +591,9 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
         return;
     }
     // this CTA finishes the elements of threads rank * tpc .. of every CTA
-    const uint32_t tpc = PT_THREADS / n_cta;
-    for (uint32_t x = threadIdx.x; x < tpc * C::EPT; x += PT_THREADS) {
+    const uint32_t tpc = (PT_THREADS + n_cta - 1) / n_cta;
+    const uint32_t own = min(tpc, PT_THREADS - min(rank * tpc, (uint32_t)PT_THREADS));
+    for (uint32_t x = threadIdx.x; x < own * C::EPT; x += PT_THREADS) {
         const uint32_t t = rank * tpc + x / C::EPT, i = x % C::EPT;
         const int cb = t & 63, pt = t >> 6, hh = 2 * (cb >> 3 & 3) + (cb >> 5), rr = cb & 7;
         const int dd = (E4M3 ? rr * (D / 8) + pt * C::EPT
