@@ -133,6 +133,23 @@ def _load():
 _lib = _load()
 
 
+def _load_binding():
+    """The compiled binding of the paged cache's per-token calls, or None when it was built for
+    another torch (their Python path then serves)."""
+    try:
+        from . import _paged_binding as b
+    except ImportError:
+        return None
+    if b.torch_version != torch.__version__:
+        return None
+    b.bind(*[ctypes.cast(f, ctypes.c_void_p).value
+             for f in (_lib.lsa_paged_append, _lib.lsa_paged_attn)])
+    return b
+
+
+_binding = _load_binding()
+
+
 def library_path():
     return _LIB_PATH
 
@@ -696,6 +713,7 @@ class LsaPagedKV:
                           self.status.data_ptr(), self.B, n_pages, page_table.shape[1], page, Hkv,
                           d, fmt)
         self._ref = ctypes.byref(self._c)
+        self._addr = ctypes.addressof(self._c)
 
     @classmethod
     def empty(cls, B, n_pages, page, max_pages, Hkv, d, dtype=torch.bfloat16, device="cuda"):
@@ -788,6 +806,13 @@ def lsa_paged_append(cache, k, v, start, n_new=None, q=None, q_out=None, inv_fre
     rotation); tokens at and after n_new[b] are padding.  With q [B][Nq][Hq][d] the queries are
     rotated too: into q_out (which may be q; rows of padding are left as they are) or a new
     tensor, which is returned (None without q).  C: lsa_paged_append."""
+    if stream is None and _binding is not None:
+        r = _binding.append(cache._addr, cache._index, k, v, start, n_new, q, q_out, inv_freq,
+                            interleaved)
+        if r is not NotImplemented:
+            if type(r) is int:
+                _check(r)
+            return r
     if stream is not None or _current_device() != cache._index:
         with _elsewhere(cache, stream):
             return lsa_paged_append(cache, k, v, start, n_new, q, q_out, inv_freq, interleaved)
@@ -825,6 +850,12 @@ def lsa_paged_attn(cache, Q, indices, counts, scale=None, return_lse=False, out=
     """Attention of Q [B][Nq][Hq][d] (bfloat16) over the listed positions of the paged cache
     (C: lsa_paged_attn): indices [B][Nq][s_max], counts [B][Nq] int32, as the selections return
     them.  A row of count 0 gives 0 (lse -inf)."""
+    if stream is None and _binding is not None:
+        r = _binding.attn(cache._addr, cache._index, Q, indices, counts, scale, return_lse, out)
+        if r is not NotImplemented:
+            if type(r) is int:
+                _check(r)
+            return r
     if stream is not None or _current_device() != cache._index:
         with _elsewhere(cache, stream):
             return lsa_paged_attn(cache, Q, indices, counts, scale, return_lse, out)

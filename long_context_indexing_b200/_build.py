@@ -4,12 +4,18 @@ Each .cu under csrc/ is compiled to an object in parallel, then linked into
 long_context_indexing_b200/liblsa.so.  The library depends only on the CUDA
 driver at run time (the runtime is linked statically), so loading it on a
 host without a GPU succeeds; the first CUDA call then fails cleanly.
+
+csrc/py/paged_binding.cpp, the binding of the paged cache's per-token calls, is
+compiled against the installed torch and Python into _paged_binding.so beside it.
 """
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
+import re
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -17,6 +23,9 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "liblsa.so")
+BINDING_SRC = os.path.join(CSRC, "py", "paged_binding.cpp")
+BINDING = os.path.join(PKG, "_paged_binding.so")
+CXX = os.environ.get("CXX", "g++")
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -52,6 +61,27 @@ def _compile(src, verbose_ptxas=False):
     return obj, r.stderr
 
 
+def _build_binding(force=False):
+    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    version_py = os.path.join(torch_dir, "version.py")
+    if not force and not _stale(BINDING, [BINDING_SRC, version_py, *_headers()]):
+        return
+    with open(version_py) as f:
+        version = re.search(r"__version__ = ['\"]([^'\"]+)['\"]", f.read()).group(1)
+    tmp = BINDING + ".tmp.%d" % os.getpid()
+    inc = os.path.join(torch_dir, "include")
+    cmd = [CXX, "-O2", "-fPIC", "-shared", "-std=c++17", '-DLSA_TORCH_VERSION="%s"' % version,
+           "-I", INCLUDE, "-I", inc, "-I", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"],
+           "-I", os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include"), BINDING_SRC,
+           "-o", tmp, "-L", os.path.join(torch_dir, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+           "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("binding failed:\n%s%s" % (r.stdout, r.stderr))
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     """Compiles every CUDA source for sm_100a and links liblsa.so."""
     os.makedirs(BUILD, exist_ok=True)
@@ -61,8 +91,10 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
             o = os.path.join(BUILD, os.path.basename(s) + ".o")
             if os.path.exists(o):
                 os.remove(o)
-    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
+        binding = ex.submit(_build_binding, force)
         results = list(ex.map(lambda s: _compile(s, verbose_ptxas), srcs))
+        binding.result()
     objs = [o for o, _ in results]
     if verbose_ptxas:
         for (_, log), s in zip(results, srcs):

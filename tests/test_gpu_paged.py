@@ -666,3 +666,40 @@ def test_decode_step_captured_and_replayed():
         assert torch.equal(out, want[t]), t
     c.check()
     idx.check()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, FP8])
+def test_compiled_binding_and_python_path_agree(dtype, monkeypatch):
+    # the same bits through the compiled binding and through the Python path, with slices,
+    # padding, given and new outputs
+    rng = np.random.default_rng(51)
+    B, Nq, Hq, Hkv, d, page, mp = 3, 9, 12, 4, 64, 16, 6
+    base = _cache(rng, B, Hkv, d, page, mp, dtype)
+    q, k, v = _new(rng, B, Nq, Hq + 2 * Hkv, d).cuda().split([Hq, Hkv, Hkv], 2)
+    start = torch.tensor([3, 40, 80], dtype=torch.int32, device="cuda")
+    n_new = torch.tensor([9, 4, 0], dtype=torch.int32, device="cuda")
+    inv = torch.from_numpy(_freq(32)).cuda()
+    idx, cnt = (torch.from_numpy(x).cuda() for x in _rows(rng, B, Nq, mp * page, 50, [50, 0, 7]))
+    assert lsa._binding is not None
+    got = []
+    for path in range(2):
+        if path:
+            monkeypatch.setattr(lsa, "_binding", None)
+        c = lsa.LsaPagedKV(base.k_pages.clone(), base.v_pages.clone(), base.page_table,
+                           None if base.scales is None else base.scales.clone())
+        qr = lsa.lsa_paged_append(c, k, v, start, q=q, inv_freq=inv, interleaved=True)
+        given = torch.zeros_like(qr)
+        assert lsa.lsa_paged_append(c, k, v, start, n_new=n_new, q=q, q_out=given) is given
+        assert lsa.lsa_paged_append(c, k, v, start) is None
+        O, lse = lsa.lsa_paged_attn(c, qr, idx, cnt, scale=0.3, return_lse=True)
+        P = torch.zeros_like(O)
+        assert lsa.lsa_paged_attn(c, qr, idx, cnt, out=P) is P
+        one = lsa.lsa_paged_attn(c, qr, idx, cnt)
+        c.check()
+        got.append([qr, given, O, lse, P, one, c.k_pages.view(torch.uint8), c.v_pages.view(torch.uint8)]
+                   + ([] if c.scales is None else [c.scales]))
+        with pytest.raises(lsa.LsaError) as e:                  # refused by the C entry
+            lsa.lsa_paged_attn(c, qr, idx, cnt, scale=-1.0)
+        assert e.value.code == 1
+    for x, y in zip(*got):
+        assert x.dtype == y.dtype and x.shape == y.shape and torch.equal(x, y)

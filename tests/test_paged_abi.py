@@ -118,6 +118,23 @@ def test_decode_step_arguments_refused():
     assert f(h, ctypes.byref(_kv()), 8, lsa.SelectParams(-1, 64, 4)) == 0
 
 
+def test_binding_is_built_for_this_torch_and_steps_aside():
+    # wrong arguments of every kind come back as NotImplemented, for the Python path to name
+    b = lsa._binding
+    assert b is not None and b.torch_version == torch.__version__
+    k = torch.zeros(2, 1, 2, 64, dtype=torch.bfloat16)
+    i = torch.zeros(2, 1, 3, dtype=torch.int32)
+    kv = _kv(d=64)
+    addr = ctypes.addressof(kv)
+    for args in ((addr, 0, k, k, i, None, None, None, None, False), (addr, 0, 1, 2, 3, 4, 5, 6, 7, 8),
+                 (addr, 0), (0, 0, k, k, i, None, None, None, None, False)):
+        if torch.cuda.is_available() or args[0] == 0 or len(args) != 10:
+            assert b.append(*args) is NotImplemented
+    assert b.attn(addr, 0) is NotImplemented
+    with pytest.raises(TypeError):
+        b.bind(1)
+
+
 def test_handle_wants_cuda_tensors_of_one_kind():
     k = torch.zeros(4, 16, 2, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError):
