@@ -29,7 +29,7 @@
 // MB, 6.25 TB/s, 0.95 of a copy's rate: HBM); 2 x 4,096 tokens of 16/2 heads into
 // bf16 pages 18.3 us (4.6 TB/s; 514 CTAs, a little over one wave of 444); 7 padded
 // prompts of up to 1,021 tokens of 24/8 heads of 64 10.7 us (waves of latencies:
-// start 1.0 us, page and turns 2, keys and values 3.6, queries 2.8); 8 tokens 3.5 us.
+// start 1.0 us, page and turns 2, keys and values 3.6, queries 2.8); 8 tokens 3.1 us.
 #include "paged.cuh"
 #include "ptx.cuh"
 
@@ -143,6 +143,7 @@ __global__ void __launch_bounds__(PA_THREADS, 3) paged_append_kernel(lsa_paged_k
     constexpr int TURN_ROW = D / 2 + (D == 64 ? 16 : 0);
     __shared__ __align__(16) float cos_s[SCALE_BLOCK][TURN_ROW], sin_s[SCALE_BLOCK][TURN_ROW];
     __shared__ uint4 raw_s[PA_WARPS][QB][2][32];         // what a lane reads, NP or QB pairs
+    ptx::grid_dependency();
     // one CTA for a block's keys, values and queries, or one for each part
     const bool do_kv = blockIdx.z == 0, do_q = a.Hq > 0 && blockIdx.z == gridDim.z - 1;
     const int64_t b = blockIdx.y;
@@ -397,11 +398,22 @@ cudaError_t launch_paged_append(const lsa_paged_kv& kv, const AppendArgs& a, cud
     // than the shorter CTAs bring (32,768 tokens 101 us against 107)
     const bool split = a.Hq > 0 && blocks * kv.B <= 2 * 3 * (int64_t)sm_count();
     const dim3 grid((unsigned)blocks, (unsigned)kv.B, split ? 2u : 1u);
-    auto run = [&](auto kern) { kern<<<grid, PA_THREADS, 0, st>>>(kv, a); };
+    auto run = [&](auto kern) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = grid;
+        cfg.blockDim = dim3(PA_THREADS);
+        cfg.stream = st;
+        cudaLaunchAttribute at = dependent_launch();
+        cfg.attrs = &at;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, kern, kv, a);
+    };
+    cudaError_t e;
     if (kv.format == LSA_KV_E4M3)
-        kv.d == 64 ? run(paged_append_kernel<true, 64>) : run(paged_append_kernel<true, 128>);
+        e = kv.d == 64 ? run(paged_append_kernel<true, 64>) : run(paged_append_kernel<true, 128>);
     else
-        kv.d == 64 ? run(paged_append_kernel<false, 64>) : run(paged_append_kernel<false, 128>);
+        e = kv.d == 64 ? run(paged_append_kernel<false, 64>) : run(paged_append_kernel<false, 128>);
+    if (e != cudaSuccess) return e;
     note_launch();
     return cudaGetLastError();
 }

@@ -42,8 +42,8 @@
 // memory, one barrier).
 //
 // Bound and measured (B200, 32/4 heads of 128 unless said): 8 rows of 4,612 keys,
-// 8-bit, 14.6 us, of which 3.6 before the first product (positions, pages, rows:
-// three dependent reads) and 3 in the merge; 32 rows 34 us (4.5 TB/s); 64 rows of
+// 8-bit, 13.5 us, of which 3.6 before the first product (positions, pages, rows:
+// three dependent reads) and 3 in the merge; 32 rows 33 us (4.6 TB/s); 64 rows of
 // 16/2 heads in bf16 pages 52 us (5.8 TB/s, 0.89 of a copy's rate: HBM); 251 rows
 // of 16/2 heads over 128k in bf16 pages 120 us (9.9 TB/s of rows, most of them from
 // L2); 1,024 rows of 2,564 keys over 1M, 8-bit, 360 us (7.6 TB/s of rows: HBM, for
@@ -187,6 +187,7 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
     uint32_t rank, n_cta;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(n_cta));
+    ptx::grid_dependency();
     // the CTAs of the cluster have started before any is written to
     if (n_cta > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -655,10 +656,6 @@ cudaError_t launch_paged_attn(const lsa_paged_kv& kv, const void* Q, int64_t Nq,
     auto run = [&](auto kern, int bytes) {
         cudaError_t e = ensure_smem_attr((const void*)kern, bytes);
         if (e != cudaSuccess) return e;
-        if (c == 1) {
-            kern<<<(unsigned)units, PT_THREADS, bytes, st>>>(kv, a);
-            return cudaGetLastError();
-        }
         if (c > 8) {
             e = cudaFuncSetAttribute((const void*)kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
             if (e != cudaSuccess) return e;
@@ -668,12 +665,12 @@ cudaError_t launch_paged_attn(const lsa_paged_kv& kv, const void* Q, int64_t Nq,
         cfg.blockDim = dim3(PT_THREADS);
         cfg.dynamicSmemBytes = bytes;
         cfg.stream = st;
-        cudaLaunchAttribute at;
-        at.id = cudaLaunchAttributeClusterDimension;
-        at.val.clusterDim.x = (unsigned)c;
-        at.val.clusterDim.y = at.val.clusterDim.z = 1;
-        cfg.attrs = &at;
-        cfg.numAttrs = 1;
+        cudaLaunchAttribute at[2] = {dependent_launch()};
+        at[1].id = cudaLaunchAttributeClusterDimension;
+        at[1].val.clusterDim.x = (unsigned)c;
+        at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = c > 1 ? 2 : 1;
         return cudaLaunchKernelEx(&cfg, kern, kv, a);
     };
     cudaError_t e;

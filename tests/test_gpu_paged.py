@@ -703,3 +703,38 @@ def test_compiled_binding_and_python_path_agree(dtype, monkeypatch):
         assert e.value.code == 1
     for x, y in zip(*got):
         assert x.dtype == y.dtype and x.shape == y.shape and torch.equal(x, y)
+
+
+def test_calls_in_a_row_wait_for_each_other():
+    # a long chain without a wait in between: each step appends what the attention before it
+    # wrote, among torch's own kernels; the same as with a wait after every call
+    rng = np.random.default_rng(61)
+    B, Hq, Hkv, d, page, mp = 6, 16, 4, 128, 16, 20
+    base = _cache(rng, B, Hkv, d, page, mp, FP8)
+    x0 = _new(rng, B, 1, Hq, d).cuda()
+    inv = torch.from_numpy(_freq(128)).cuda()
+    idx, cnt = (torch.from_numpy(x).cuda() for x in _rows(rng, B, 1, mp * page, 300, [300, 40, 0, 299]))
+
+    def chain(wait):
+        c = lsa.LsaPagedKV(base.k_pages.clone(), base.v_pages.clone(), base.page_table,
+                           base.scales.clone())
+        x, pos = x0.clone(), torch.arange(B, dtype=torch.int32, device="cuda") * 3
+        out = []
+        for step in range(60):
+            qr = lsa.lsa_paged_append(c, x[:, :, :Hkv], x[:, :, Hkv:2 * Hkv], pos, q=x, inv_freq=inv)
+            if wait:
+                torch.cuda.synchronize()
+            x = lsa.lsa_paged_attn(c, qr, idx, cnt)
+            if step % 3 == 0:
+                x = (x * 1.5 + x0).clamp_(-8, 8)
+            pos += 1
+            if wait:
+                torch.cuda.synchronize()
+            out.append(x)
+        torch.cuda.synchronize()
+        return torch.stack(out), c.k_pages.view(torch.uint8)
+
+    a, ka = chain(True)
+    for _ in range(3):
+        b, kb = chain(False)
+        assert torch.equal(a, b) and torch.equal(ka, kb)
