@@ -394,7 +394,7 @@ cudaError_t launch_paged_append(const lsa_paged_kv& kv, const AppendArgs& a, cud
     // Nq consecutive positions touch at most (Nq + 14) / 16 + 1 blocks
     const int64_t blocks = (a.Nq + SCALE_BLOCK - 2) / SCALE_BLOCK + 1;
     // up to two waves the queries get CTAs of their own (8 tokens 4.2 us against 3.5,
-    // 7 padded prompts 11.5 against 10.7); past that the turns computed twice cost more
+    // 7 padded prompts 11.5 against 10.2); past that the turns computed twice cost more
     // than the shorter CTAs bring (32,768 tokens 101 us against 107)
     const bool split = a.Hq > 0 && blocks * kv.B <= 2 * 3 * (int64_t)sm_count();
     const dim3 grid((unsigned)blocks, (unsigned)kv.B, split ? 2u : 1u);

@@ -738,3 +738,92 @@ def test_calls_in_a_row_wait_for_each_other():
     for _ in range(3):
         b, kb = chain(False)
         assert torch.equal(a, b) and torch.equal(ka, kb)
+
+
+def test_calls_wait_for_other_streams_copies_and_fills():
+    # inputs that a slow side stream, a copy and a fill have just written, joined by events,
+    # eagerly and as branches of a captured graph: the same as with a wait after everything
+    rng = np.random.default_rng(67)
+    B, Hq, Hkv, d, page, mp = 5, 16, 4, 128, 32, 12
+    base = _cache(rng, B, Hkv, d, page, mp, FP8)
+    k0, v0, q0 = (_new(rng, B, 2, h, d).cuda() for h in (Hkv, Hkv, Hq))
+    inv = torch.from_numpy(_freq(128)).cuda()
+    idx0, cnt0 = (torch.from_numpy(x).cuda() for x in _rows(rng, B, 2, mp * page, 90, [90, 0, 33]))
+    side = torch.cuda.Stream()
+    main = torch.cuda.Stream()
+
+    def step(c, b, sync):
+        here = torch.cuda.current_stream()
+        wait = torch.cuda.synchronize if sync else (lambda: None)
+        b["start"].fill_(7)                             # a fill straight before
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(200000)
+            b["k"].copy_(k0)
+            b["v"].copy_(v0 * 2)
+        b["q"].copy_(q0)                                # beside the branch
+        wait()
+        here.wait_stream(side)
+        qr = lsa.lsa_paged_append(c, b["k"], b["v"], b["start"], q=b["q"], inv_freq=inv)
+        wait()
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(200000)
+            b["idx"].copy_(idx0)
+        b["cnt"].copy_(cnt0)
+        here.wait_stream(side)
+        wait()
+        O, l = lsa.lsa_paged_attn(c, qr, b["idx"], b["cnt"], return_lse=True)
+        wait()
+        b["k"].zero_(), b["q"].zero_(), b["idx"].fill_(-1), b["cnt"].zero_()
+        return O, l
+
+    def fresh():
+        c = lsa.LsaPagedKV(base.k_pages.clone(), base.v_pages.clone(), base.page_table,
+                           base.scales.clone())
+        b = dict(k=torch.zeros_like(k0), v=torch.zeros_like(v0), q=torch.zeros_like(q0),
+                 idx=torch.full_like(idx0, -1), cnt=torch.zeros_like(cnt0),
+                 start=torch.zeros(B, dtype=torch.int32, device="cuda"))
+        torch.cuda.synchronize()
+        return c, b
+
+    with torch.cuda.stream(main):
+        c0, b0 = fresh()
+        O0, l0 = step(c0, b0, True)
+        c1, b1 = fresh()
+        for _ in range(4):
+            O, l = step(c1, b1, False)
+            torch.cuda.synchronize()
+            assert torch.equal(O, O0) and torch.equal(l, l0)
+    c2, b2 = fresh()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=main):
+        Og, lg = step(c2, b2, False)
+    for _ in range(4):
+        Og.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(Og, O0) and torch.equal(lg, l0)
+    for c in (c1, c2):
+        c.check()
+        assert torch.equal(c.k_pages.view(torch.uint8), c0.k_pages.view(torch.uint8))
+        assert torch.equal(c.v_pages.view(torch.uint8), c0.v_pages.view(torch.uint8))
+
+
+def test_attention_of_a_position_listed_many_times():
+    # every listing counts: a position listed n times weighs n times, within a tile and across
+    # the tiles, warps and CTAs of a row
+    rng = np.random.default_rng(71)
+    for dtype in (torch.bfloat16, FP8):
+        c = _cache(rng, 1, 2, 128, 32, 4, dtype)
+        Q = _new(rng, 1, 3, 10, 128).cuda()
+        idx = np.full((1, 3, 2000), -1, np.int32)
+        idx[0, 0] = 5                                   # one position only
+        idx[0, 1] = rng.choice([3, 64, 127], 2000)
+        idx[0, 2, ::2] = 9
+        idx[0, 2, 1::2] = np.arange(1000) % 128
+        cnt = np.full((1, 3), 2000, np.int32)
+        O, l = lsa.lsa_paged_attn(c, Q, torch.from_numpy(idx).cuda(), torch.from_numpy(cnt).cuda(),
+                                  return_lse=True)
+        c.check()
+        _check_attn(c, Q, idx, cnt, 128 ** -0.5, O, l)
