@@ -27,8 +27,8 @@
 // two the keys' part waits (32,768 tokens of 4 heads 45 us against 38).
 // Measured (B200): 32,768 tokens of 32/4 heads of 128 into 8-bit pages 102 us (637.6
 // MB, 6.25 TB/s, 0.95 of a copy's rate: HBM); 2 x 4,096 tokens of 16/2 heads into
-// bf16 pages 18.3 us (4.6 TB/s; 514 CTAs, a little over one wave of 444); 7 padded
-// prompts of up to 1,021 tokens of 24/8 heads of 64 10.7 us (waves of latencies:
+// bf16 pages 17.9 us (4.7 TB/s; 514 CTAs, a little over one wave of 444); 7 padded
+// prompts of up to 1,021 tokens of 24/8 heads of 64 9.8 us (waves of latencies:
 // start 1.0 us, page and turns 2, keys and values 3.6, queries 2.8); 8 tokens 3.1 us.
 #include "paged.cuh"
 #include "ptx.cuh"

@@ -45,8 +45,8 @@
 // 8-bit, 13.5 us, of which 3.6 before the first product (positions, pages, rows:
 // three dependent reads) and 3 in the merge; 32 rows 33 us (4.6 TB/s); 64 rows of
 // 16/2 heads in bf16 pages 52 us (5.8 TB/s, 0.89 of a copy's rate: HBM); 251 rows
-// of 16/2 heads over 128k in bf16 pages 120 us (9.9 TB/s of rows, most of them from
-// L2); 1,024 rows of 2,564 keys over 1M, 8-bit, 360 us (7.6 TB/s of rows: HBM, for
+// of 16/2 heads over 128k in bf16 pages 104 us (11.4 TB/s of rows, most of them from
+// L2); 1,024 rows of 2,564 keys over 1M, 8-bit, 395 us (6.8 TB/s of rows: HBM, for
 // rows that list the same bucket seldom run together).  With all warps busy a
 // 16-key stage of 8-bit rows issues about 285 instructions, 135 of them on the ALU
 // pipe (64 conversions), at 55 to 60 % of the issue slots; CTAs of 8 warps, stages
@@ -100,6 +100,8 @@ struct PagedAttnArgs {
     int s_max;
     int page_shift;
     float scale_log2;                // scale * log2(e)
+    int64_t unit0;                   // this launch's first unit
+    bool leads, follows;             // the first, the second launch of a call with two
     __nv_bfloat16* O;
     float* lse;
 };
@@ -187,12 +189,16 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
     uint32_t rank, n_cta;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(n_cta));
-    ptx::grid_dependency();
+    // A second launch starts as the first one's CTAs end: those have waited for all that
+    // came before, and it waits for them before it ends, so that whoever waits for the
+    // second has waited for both.
+    if (!a.follows) ptx::grid_dependency();
+    if (a.leads) ptx::grid_release();
     // the CTAs of the cluster have started before any is written to
     if (n_cta > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r8 = lane >> 2, t4 = lane & 3;
-    const int64_t unit = blockIdx.x / n_cta;
+    const int64_t unit = a.unit0 + blockIdx.x / n_cta;
     const int upr = kv.Hkv * a.chunks;                 // units per row
     const int64_t row = unit / upr;
     const int g = (int)(unit % upr) / a.chunks;
@@ -589,6 +595,7 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
             if (a.lse && dim == 0)
                 a.lse[hbase + h] = L == 0.f ? -INFINITY : (M1 + log2f(L)) * 0.6931471805599453f;
         }
+        if (a.follows) ptx::grid_dependency();
         return;
     }
     // this CTA finishes the elements of threads rank * tpc .. of every CTA
@@ -617,6 +624,7 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
                 a.lse[hbase + hh] = S == 0.f ? -INFINITY : (N1 + log2f(S)) * 0.6931471805599453f;
         }
     }
+    if (a.follows) ptx::grid_dependency();
 }
 
 cudaError_t launch_paged_attn(const lsa_paged_kv& kv, const void* Q, int64_t Nq, int Hq,
@@ -646,32 +654,62 @@ cudaError_t launch_paged_attn(const lsa_paged_kv& kv, const void* Q, int64_t Nq,
     // units: 58.8 us with one, 75.1 with 2).  Clusters of 16 find fewer places in
     // the GPCs (32 units: 14.6 us with 8, 22.7 with 16, of which 31 fit).
     const int64_t slots = (int64_t)sm_count() * (kv.format == LSA_KV_BF16 && kv.d == 128 ? 3 : 4);
-    int c = 1;
-    while (c < PT_MAX_C) {
-        const int64_t ctas = units * c * 2;
-        const int64_t tiles = s_max / (2 * c * PT_WARPS * 32);     // per warp after the split
-        if (tiles < 1 || ctas > (c == 8 ? slots / 4 : tiles < 6 ? slots / 2 : slots)) break;
-        c *= 2;
-    }
+    auto split = [&](int64_t n) {
+        int c = 1;
+        while (c < PT_MAX_C) {
+            const int64_t ctas = n * c * 2;
+            const int64_t tiles = s_max / (2 * c * PT_WARPS * 32);  // per warp after the split
+            if (tiles < 1 || ctas > (c == 8 ? slots / 4 : tiles < 6 ? slots / 2 : slots)) break;
+            c *= 2;
+        }
+        return c;
+    };
+    // Units past the last whole wave would run alone for as long as a full wave's.  Where
+    // they fill less than 3/8 of one they follow in a launch of their own, split like a
+    // small call's, that starts on the places that the first launch leaves (502 bf16
+    // units of 4,612 keys: 129 us in one launch, 108 in two; 640 8-bit units of 2,564
+    // keys 85.6 against 71; 1,240 units 140 against 129).  With more of them there is
+    // little to win (700 bf16 units 149.5 against 154), nor with short rows (596 units of
+    // 260 keys 15.5 against 17.2; of 1,156 keys 37.8 against 32.2) or after many waves
+    // (6,000 units 602 either way).  Rows of unequal length fill the last wave by
+    // themselves and lose by it (640 units of 0 to 2,564 keys 42.1 against 44.8), but
+    // only the device knows their counts.
+    const int64_t rest = units > slots && units < 8 * slots && s_max >= 1024 ? units % slots : 0;
+    const int64_t behind = rest <= slots * 3 / 8 ? rest : 0;
     auto run = [&](auto kern, int bytes) {
         cudaError_t e = ensure_smem_attr((const void*)kern, bytes);
         if (e != cudaSuccess) return e;
-        if (c > 8) {
-            e = cudaFuncSetAttribute((const void*)kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-            if (e != cudaSuccess) return e;
-        }
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)(units * c));
-        cfg.blockDim = dim3(PT_THREADS);
-        cfg.dynamicSmemBytes = bytes;
-        cfg.stream = st;
-        cudaLaunchAttribute at[2] = {dependent_launch()};
-        at[1].id = cudaLaunchAttributeClusterDimension;
-        at[1].val.clusterDim.x = (unsigned)c;
-        at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
-        cfg.attrs = at;
-        cfg.numAttrs = c > 1 ? 2 : 1;
-        return cudaLaunchKernelEx(&cfg, kern, kv, a);
+        auto launch = [&](int64_t n) {
+            const int c = split(n);
+            if (c > 8) {
+                e = cudaFuncSetAttribute((const void*)kern,
+                                         cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+                if (e != cudaSuccess) return e;
+            }
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3((unsigned)(n * c));
+            cfg.blockDim = dim3(PT_THREADS);
+            cfg.dynamicSmemBytes = bytes;
+            cfg.stream = st;
+            cudaLaunchAttribute at[2] = {dependent_launch()};
+            at[1].id = cudaLaunchAttributeClusterDimension;
+            at[1].val.clusterDim.x = (unsigned)c;
+            at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+            cfg.attrs = at;
+            cfg.numAttrs = c > 1 ? 2 : 1;
+            e = cudaLaunchKernelEx(&cfg, kern, kv, a);
+            if (e == cudaSuccess) note_launch();
+            return e;
+        };
+        a.unit0 = 0;
+        a.leads = behind > 0;
+        a.follows = false;
+        e = launch(units - behind);
+        if (e != cudaSuccess || behind == 0) return e;
+        a.unit0 = units - behind;
+        a.leads = false;
+        a.follows = true;
+        return launch(behind);
     };
     cudaError_t e;
     if (kv.format == LSA_KV_E4M3)
@@ -680,9 +718,7 @@ cudaError_t launch_paged_attn(const lsa_paged_kv& kv, const void* Q, int64_t Nq,
     else
         e = kv.d == 64 ? run(paged_attn_kernel<false, 64>, PagedCfg<false, 64>::BYTES)
                        : run(paged_attn_kernel<false, 128>, PagedCfg<false, 128>::BYTES);
-    if (e != cudaSuccess) return e;
-    note_launch();
-    return cudaGetLastError();
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace lsa

@@ -8,9 +8,10 @@ namespace lsa {
 // The kernel is set up while the one before it on the stream still runs and waits
 // for that one before it reads or writes anything (ptx::grid_dependency): calls in
 // a row are 1 to 2 us closer (8 tokens' append 5.1 us a call against 3.1, a 33-row
-// attention 10.2 against 8.1).  None lets its successor start before it ends: blocks
+// attention 10.2 against 8.1).  None lets a later call start before it ends: blocks
 // that wait on an SM leave the next grid unevenly spread (64 rows in bf16 pages
-// 52.0 us against 56.6 and more).
+// 52.0 us against 56.6 and more); only the second launch of one attention call
+// starts on the places that the first one leaves.
 inline cudaLaunchAttribute dependent_launch()
 {
     cudaLaunchAttribute at;

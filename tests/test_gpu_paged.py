@@ -827,3 +827,87 @@ def test_attention_of_a_position_listed_many_times():
                                   return_lse=True)
         c.check()
         _check_attn(c, Q, idx, cnt, 128 ** -0.5, O, l)
+
+
+@pytest.mark.parametrize("dtype,B,Nq,Hq,Hkv,d", [(torch.bfloat16, 1, 225, 6, 2, 128),
+                                                 (FP8, 3, 50, 4, 4, 128), (FP8, 203, 1, 9, 3, 64),
+                                                 (torch.bfloat16, 1, 70, 80, 1, 64),
+                                                 (torch.bfloat16, 90, 10, 2, 1, 128)])
+def test_attention_in_two_launches(dtype, B, Nq, Hq, Hkv, d):
+    # a little more than one or two waves of units: the last ones run in a launch of their own
+    rng = np.random.default_rng(73)
+    page, mp, s = 16, 6, 1030
+    c = _cache(rng, B, Hkv, d, page, mp, dtype)
+    Q = _new(rng, B, Nq, Hq, d).cuda()
+    idx, cnt = _rows(rng, B, Nq, mp * page, s, [1030, 1, 0, 700, 1029, 513, 96])
+    before = lsa.kernel_launches()
+    O, l = lsa.lsa_paged_attn(c, Q, torch.from_numpy(idx).cuda(), torch.from_numpy(cnt).cuda(),
+                              return_lse=True)
+    assert lsa.kernel_launches() == before + 2
+    c.check()
+    _check_attn(c, Q, idx, cnt, d ** -0.5, O, l)
+
+
+def test_two_launches_are_waited_for_and_wait():
+    # attention in two launches between calls that write what it reads and read what it writes,
+    # eagerly and captured: the same as with a wait after every call
+    rng = np.random.default_rng(79)
+    B, Nq, Hq, Hkv, d, page, mp, s = 1, 150, 8, 4, 128, 32, 24, 1100
+    base = _cache(rng, B, Hkv, d, page, mp, FP8)
+    x0 = _new(rng, B, Nq, Hq, d).cuda()
+    inv = torch.from_numpy(_freq(128)).cuda()
+    cnt = np.full((B, Nq), s, np.int32)
+    idx = rng.integers(0, mp * page, (B, Nq, s)).astype(np.int32)
+    # the first launch's rows long, the last ones' short: the second launch ends early
+    cnt[:, 148:] = 3
+    idx, cnt = torch.from_numpy(idx).cuda(), torch.from_numpy(cnt).cuda()
+    pos = torch.tensor([1], dtype=torch.int32, device="cuda")
+
+    def chain(c, wait, steps):
+        x, out = x0.clone(), []
+        for step in range(steps):
+            qr = lsa.lsa_paged_append(c, x[:, :, :Hkv], x[:, :, Hkv:], pos + step, q=x,
+                                      inv_freq=inv)
+            if wait:
+                torch.cuda.synchronize()
+            x = lsa.lsa_paged_attn(c, qr, idx, cnt)
+            if wait:
+                torch.cuda.synchronize()
+            if step % 3 == 1:
+                x = (x * 1.5 + x0).clamp_(-8, 8)
+            if step % 4 == 2:
+                qr.zero_()                              # (its launches have read it)
+                x = lsa.lsa_paged_attn(c, x, idx, cnt)
+            if wait:
+                torch.cuda.synchronize()
+            out.append(x)
+        return torch.stack(out)
+
+    def copy():
+        return lsa.LsaPagedKV(base.k_pages.clone(), base.v_pages.clone(), base.page_table,
+                              base.scales.clone())
+
+    ca = copy()
+    a = chain(ca, True, 20)
+    for stream in (torch.cuda.current_stream(), torch.cuda.Stream()):
+        cb = copy()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(stream):
+            b = chain(cb, False, 20)
+        torch.cuda.synchronize()
+        assert torch.equal(a, b)
+        assert torch.equal(ca.k_pages.view(torch.uint8), cb.k_pages.view(torch.uint8))
+    cg, g = copy(), torch.cuda.CUDAGraph()
+    k, v, sc = (t.clone() for t in (cg.k_pages.view(torch.uint8), cg.v_pages.view(torch.uint8),
+                                    cg.scales))
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        out = chain(cg, False, 20)
+    for _ in range(3):
+        cg.k_pages.view(torch.uint8).copy_(k)
+        cg.v_pages.view(torch.uint8).copy_(v)
+        cg.scales.copy_(sc)
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(a, out)
