@@ -27,9 +27,9 @@
 // two the keys' part waits (32,768 tokens of 4 heads 45 us against 38).
 // Measured (B200): 32,768 tokens of 32/4 heads of 128 into 8-bit pages 102 us (637.6
 // MB, 6.25 TB/s, 0.95 of a copy's rate: HBM); 2 x 4,096 tokens of 16/2 heads into
-// bf16 pages 17.9 us (4.7 TB/s; 514 CTAs, a little over one wave of 444); 7 padded
-// prompts of up to 1,021 tokens of 24/8 heads of 64 9.8 us (waves of latencies:
-// start 1.0 us, page and turns 2, keys and values 3.6, queries 2.8); 8 tokens 3.1 us.
+// bf16 pages 16.2 us (5.2 TB/s; 514 blocks, the queries in CTAs of their own); 7 padded
+// prompts of up to 1,021 tokens of 24/8 heads of 64 10 us (waves of latencies:
+// start 1.0 us, page and turns 2, keys and values 3.6, queries 2.8); 256 tokens of 32/4 heads 4.2 us, 8 tokens 3.1.
 #include "paged.cuh"
 #include "ptx.cuh"
 
@@ -144,8 +144,11 @@ __global__ void __launch_bounds__(PA_THREADS, 3) paged_append_kernel(lsa_paged_k
     __shared__ __align__(16) float cos_s[SCALE_BLOCK][TURN_ROW], sin_s[SCALE_BLOCK][TURN_ROW];
     __shared__ uint4 raw_s[PA_WARPS][QB][2][32];         // what a lane reads, NP or QB pairs
     ptx::grid_dependency();
-    // one CTA for a block's keys, values and queries, or one for each part
-    const bool do_kv = blockIdx.z == 0, do_q = a.Hq > 0 && blockIdx.z == gridDim.z - 1;
+    // one CTA for a block's keys, values and queries; or one for the queries and then one
+    // for the rest; or one for the rest and several for the queries' heads
+    const int parts = max((int)gridDim.z - 1, 1);        // of the queries
+    const int kv_z = gridDim.z == 2 ? 1 : 0;
+    const bool do_kv = (int)blockIdx.z == kv_z, do_q = a.Hq > 0 && (gridDim.z == 1 || !do_kv);
     const int64_t b = blockIdx.y;
     const int64_t start = a.start[b];
     int64_t n = a.n_new ? a.n_new[b] : a.Nq;
@@ -200,6 +203,26 @@ __global__ void __launch_bounds__(PA_THREADS, 3) paged_append_kernel(lsa_paged_k
         ptx::cp_async_commit();
     };
     if (do_kv && warp < 2 * Hkv) ask(warp, 0);
+    // queries: a group's token and heads
+    int tp = 1;                              // token slots, a power of two
+    while (tp < i1 - i0) tp *= 2;
+    const int grp = threadIdx.x / LPT;
+    const int i = i0 + (grp & (tp - 1));
+    const int hs = GROUPS / tp * parts;
+    const int h_first = grp / tp + (gridDim.z > 2 ? (int)blockIdx.z - 1 : 0) * (GROUPS / tp);
+    auto ask_head = [&](int u, int h) {
+        const __nv_bfloat16* src = a.q + (row0 + i) * a.q_stride;
+        if (h < a.Hq) {
+            ptx::cp_async16(&raw_s[warp][u][0][lane], src + h * D + ca);
+            ptx::cp_async16(&raw_s[warp][u][1][lane], src + h * D + cb);
+        }
+        ptx::cp_async_commit();
+    };
+    auto ask_first = [&] {
+#pragma unroll
+        for (int u = 0; u < QB; ++u) ask_head(u, h_first + u * hs);
+    };
+    if (!do_kv && i < i1) ask_first();
 
     // frequency f of a token at place pos(f): a lane's four or eight turns are
     // 16-byte runs, the runs of consecutive lanes side by side
@@ -350,28 +373,15 @@ __global__ void __launch_bounds__(PA_THREADS, 3) paged_append_kernel(lsa_paged_k
     }
 
     // ---- queries: groups over (token, head), the token fixed ----
-    ptx::cp_async_wait<0>();
-    if (!do_q) return;
-    int tp = 1;                              // token slots, a power of two
-    while (tp < i1 - i0) tp *= 2;
-    const int grp = threadIdx.x / LPT;
-    const int i = i0 + (grp & (tp - 1));
-    const int hs = GROUPS / tp;
-    if (i >= i1) return;
+    if (!do_q || i >= i1) return;
     Turns r;
     if (turns) load_turns(r, i);
-    const __nv_bfloat16* src = a.q + (row0 + i) * a.q_stride;
     __nv_bfloat16* dst = a.q_out + (row0 + i) * (int64_t)a.Hq * D;
-    auto ask_head = [&](int u, int h) {
-        if (h < a.Hq) {
-            ptx::cp_async16(&raw_s[warp][u][0][lane], src + h * D + ca);
-            ptx::cp_async16(&raw_s[warp][u][1][lane], src + h * D + cb);
-        }
-        ptx::cp_async_commit();
-    };
-    int h = grp / tp;
-#pragma unroll
-    for (int u = 0; u < QB; ++u) ask_head(u, h + u * hs);
+    if (do_kv) {                             // (raw_s held keys and values)
+        ptx::cp_async_wait<0>();
+        ask_first();
+    }
+    int h = h_first;
     for (int u = 0; h < a.Hq; h += hs, u = u + 1 < QB ? u + 1 : 0) {
         ptx::cp_async_wait<QB - 1>();
         uint4 xa = raw_s[warp][u][0][lane], xb = raw_s[warp][u][1][lane];
@@ -393,11 +403,23 @@ cudaError_t launch_paged_append(const lsa_paged_kv& kv, const AppendArgs& a, cud
 {
     // Nq consecutive positions touch at most (Nq + 14) / 16 + 1 blocks
     const int64_t blocks = (a.Nq + SCALE_BLOCK - 2) / SCALE_BLOCK + 1;
-    // up to two waves the queries get CTAs of their own (8 tokens 4.2 us against 3.5,
-    // 7 padded prompts 11.5 against 10.2); past that the turns computed twice cost more
-    // than the shorter CTAs bring (32,768 tokens 101 us against 107)
-    const bool split = a.Hq > 0 && blocks * kv.B <= 2 * 3 * (int64_t)sm_count();
-    const dim3 grid((unsigned)blocks, (unsigned)kv.B, split ? 2u : 1u);
+    // Up to two waves of blocks, the queries get CTAs of their own (8 tokens 4.2 us against
+    // 3.5; past that the turns computed twice cost more than the shorter CTAs bring:
+    // 16,384 tokens 53.7 us against 54.8), and while all CTAs come to two on an SM at most
+    // their heads are cut into as many parts as one CTA's loads in flight make (256 tokens
+    // 5.8 us against 4.2; with three on an SM 1,024 tokens 5.1 against 5.7).  With one part
+    // the queries' CTAs are first, for they are the longer ones (2 x 4,096 tokens 17.6 us
+    // against 16.2); with several the keys' and values' are.
+    const int64_t ctas = blocks * kv.B;
+    int parts = 0;
+    if (a.Hq > 0 && ctas <= 2 * 3 * (int64_t)sm_count()) {
+        int tp = 1;                                      // tokens of a block at most
+        while (tp < SCALE_BLOCK && tp < a.Nq) tp *= 2;
+        const int batch = PA_THREADS * 16 / kv.d / tp * 4;     // heads a CTA has in flight
+        const int64_t most = (a.Hq + batch - 1) / batch, fit = 2 * (int64_t)sm_count() / ctas - 1;
+        parts = (int)(fit < 1 ? 1 : fit < most ? fit : most);
+    }
+    const dim3 grid((unsigned)blocks, (unsigned)kv.B, 1u + parts);
     auto run = [&](auto kern) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = grid;

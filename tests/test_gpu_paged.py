@@ -911,3 +911,16 @@ def test_two_launches_are_waited_for_and_wait():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(a, out)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, FP8])
+@pytest.mark.parametrize("B,Nq,Hq,Hkv,d,page,rot,inter,start", [
+    (1, 100, 40, 4, 128, 32, 128, False, 11),     # five parts of the queries
+    (2, 17, 21, 3, 64, 16, 32, True, 15),         # two parts, an odd number of heads
+    (1, 3, 70, 1, 128, 64, 64, False, 62),        # three parts of a few tokens
+    (18, 60, 63, 1, 128, 16, 128, False, 5),      # fewer parts than loads in flight would make
+    (40, 50, 24, 2, 128, 32, 128, True, 3),       # one part
+    (300, 20, 5, 1, 64, 16, 64, False, 0),        # keys, values and queries in one CTA
+])
+def test_append_query_parts(dtype, B, Nq, Hq, Hkv, d, page, rot, inter, start):
+    test_append(dtype, B, Nq, Hq, Hkv, d, page, rot, inter, start)
