@@ -646,23 +646,32 @@ cudaError_t launch_paged_attn(const lsa_paged_kv& kv, const void* Q, int64_t Nq,
     a.O = (__nv_bfloat16*)O;
     a.lse = lse;
     const int64_t units = kv.B * Nq * kv.Hkv * a.chunks;
-    // CTAs per unit, each with a tile per warp at least.  Up to half of the places
-    // a split shortens the rows' time (4 units of 4,612 keys: 42.3 us with one CTA,
-    // 10.9 with 8, 9.3 with 16), past that only where enough tiles are left to pay
-    // for the merge (128 units of 4,612 keys: 35.0 us with 2, 32.8 with 4; 264 units
-    // of 580 keys: 8.6 us with one, 10.3 with 2), and past one wave never (256 bf16
-    // units: 58.8 us with one, 75.1 with 2).  Clusters of 16 find fewer places in
-    // the GPCs (32 units: 14.6 us with 8, 22.7 with 16, of which 31 fit).
-    const int64_t slots = (int64_t)sm_count() * (kv.format == LSA_KV_BF16 && kv.d == 128 ? 3 : 4);
+    const int64_t sms = sm_count(), slots = sms * (kv.format == LSA_KV_BF16 && kv.d == 128 ? 3 : 4);
+    // CTAs per unit: those of the least cost by what was measured of 686 calls (2 to 512
+    // units of 100 to 8,708 keys, heads of 64 and 128, both formats), in tenths of a tile's
+    // time: a warp's tiles, each dearer by a tenth for every CTA on the SM, and the merge
+    // between CTAs, for every one on the SM.  On the mean it is within 1 % of the best
+    // choice, where splits that fill half of the places were 4 % behind it (40 units of
+    // 4,612 keys: 4 CTAs 18.9 us, 8 16.4; 128 units of 260 keys: one 6.3, two 8.8).
+    // Clusters never fill the last places (148 units of 3,016 keys: 26.7 us with two, 35.1
+    // with four, which would just fit), still less a second wave (256 bf16 units: 58.8 us
+    // with one, 75.1 with two); of 16 the GPCs have room for 31 (32 units: 14.6 us with 8,
+    // 22.7 with 16).
     auto split = [&](int64_t n) {
-        int c = 1;
-        while (c < PT_MAX_C) {
-            const int64_t ctas = n * c * 2;
-            const int64_t tiles = s_max / (2 * c * PT_WARPS * 32);  // per warp after the split
-            if (tiles < 1 || ctas > (c == 8 ? slots / 4 : tiles < 6 ? slots / 2 : slots)) break;
-            c *= 2;
+        int best = 1;
+        int64_t least = 0;
+        for (int c = 1; c <= PT_MAX_C; c *= 2) {
+            const int64_t ctas = n * c, on_sm = (ctas + sms - 1) / sms;
+            if (c > 1 && (ctas * 20 > slots * 19 || (c == 16 && n > 31))) break;
+            const int tiles = (int)(((int64_t)s_max + 32 * PT_WARPS * c - 1) / (32 * PT_WARPS * c));
+            const int64_t merge = c == 1 ? 0 : c == 2 ? 22 : c < 16 ? 18 : 27;
+            const int64_t cost = tiles * (10 + (on_sm < 4 ? on_sm : 4)) + merge * on_sm;
+            if (c == 1 || cost < least) {
+                best = c;
+                least = cost;
+            }
         }
-        return c;
+        return best;
     };
     // Units past the last whole wave would run alone for as long as a full wave's.  Where
     // they fill less than 3/8 of one they follow in a launch of their own, split like a
