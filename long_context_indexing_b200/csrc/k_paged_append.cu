@@ -410,13 +410,13 @@ cudaError_t launch_paged_append(const lsa_paged_kv& kv, const AppendArgs& a, cud
     // 5.8 us against 4.2; with three on an SM 1,024 tokens 5.1 against 5.7).  With one part
     // the queries' CTAs are first, for they are the longer ones (2 x 4,096 tokens 17.6 us
     // against 16.2); with several the keys' and values' are.
-    const int64_t ctas = blocks * kv.B;
+    const int64_t ctas = blocks * kv.B, sms = sm_count();
     int parts = 0;
-    if (a.Hq > 0 && ctas <= 2 * 3 * (int64_t)sm_count()) {
+    if (a.Hq > 0 && ctas <= 2 * 3 * sms) {
         int tp = 1;                                      // tokens of a block at most
         while (tp < SCALE_BLOCK && tp < a.Nq) tp *= 2;
         const int batch = PA_THREADS * 16 / kv.d / tp * 4;     // heads a CTA has in flight
-        const int64_t most = (a.Hq + batch - 1) / batch, fit = 2 * (int64_t)sm_count() / ctas - 1;
+        const int64_t most = (a.Hq + batch - 1) / batch, fit = 2 * sms / ctas - 1;
         parts = (int)(fit < 1 ? 1 : fit < most ? fit : most);
     }
     const dim3 grid((unsigned)blocks, (unsigned)kv.B, 1u + parts);
