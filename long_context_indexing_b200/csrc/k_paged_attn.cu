@@ -45,9 +45,9 @@
 // 8-bit, 13.5 us, of which 3.6 before the first product (positions, pages, rows:
 // three dependent reads) and 3 in the merge; 32 rows 33 us (4.6 TB/s); 64 rows of
 // 16/2 heads in bf16 pages 52 us (5.8 TB/s, 0.89 of a copy's rate: HBM); 251 rows
-// of 16/2 heads over 128k in bf16 pages 104 us (11.4 TB/s of rows, most of them from
-// L2); 1,024 rows of 2,564 keys over 1M, 8-bit, 395 us (6.8 TB/s of rows: HBM, for
-// rows that list the same bucket seldom run together).  With all warps busy a
+// of 16/2 heads over 128k in bf16 pages 104 to 113 us (10.5 to 11.4 TB/s of rows, most
+// of them from L2); 1,024 rows of 2,564 keys over 1M, 8-bit, 394 to 417 us (6.5 to 6.8
+// TB/s of rows: HBM, for rows that list the same bucket seldom run together).  With all warps busy a
 // 16-key stage of 8-bit rows issues about 285 instructions, 135 of them on the ALU
 // pipe (64 conversions), at 55 to 60 % of the issue slots; CTAs of 8 warps, stages
 // of 32 keys and L2 prefetches of later tiles were no faster.
