@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(PA_THREADS, 3) paged_append_kernel(lsa_paged_k
     constexpr int TURN_ROW = D / 2 + (D == 64 ? 16 : 0);
     __shared__ __align__(16) float cos_s[SCALE_BLOCK][TURN_ROW], sin_s[SCALE_BLOCK][TURN_ROW];
     __shared__ uint4 raw_s[PA_WARPS][QB][2][32];         // what a lane reads, NP or QB pairs
-    ptx::grid_dependency();
+    grid_dependency();
     // one CTA for a block's keys, values and queries; or one for the queries and then one
     // for the rest; or one for the rest and several for the queries' heads
     const int parts = max((int)gridDim.z - 1, 1);        // of the queries

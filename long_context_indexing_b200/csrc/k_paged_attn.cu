@@ -192,8 +192,8 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
     // A second launch starts as the first one's CTAs end: those have waited for all that
     // came before, and it waits for them before it ends, so that whoever waits for the
     // second has waited for both.
-    if (!a.follows) ptx::grid_dependency();
-    if (a.leads) ptx::grid_release();
+    if (!a.follows) grid_dependency();
+    if (a.leads) grid_release();
     // the CTAs of the cluster have started before any is written to
     if (n_cta > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -595,7 +595,7 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
             if (a.lse && dim == 0)
                 a.lse[hbase + h] = L == 0.f ? -INFINITY : (M1 + log2f(L)) * 0.6931471805599453f;
         }
-        if (a.follows) ptx::grid_dependency();
+        if (a.follows) grid_dependency();
         return;
     }
     // this CTA finishes the elements of threads rank * tpc .. of every CTA
@@ -624,7 +624,7 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
                 a.lse[hbase + hh] = S == 0.f ? -INFINITY : (N1 + log2f(S)) * 0.6931471805599453f;
         }
     }
-    if (a.follows) ptx::grid_dependency();
+    if (a.follows) grid_dependency();
 }
 
 cudaError_t launch_paged_attn(const lsa_paged_kv& kv, const void* Q, int64_t Nq, int Hq,

@@ -15,6 +15,7 @@
 
 #include "hooks.cuh"
 #include "lsa_internal.cuh"
+#include "paged.cuh"
 
 using namespace lsa;
 

@@ -65,7 +65,6 @@ enum DevErr : uint32_t {
     DEV_BAD_INDEX = 2,     // an index outside [0, T_cap) reached a gather
     DEV_FALLBACK_OVF = 3,  // fallback list overflow (cannot happen by sizing)
     DEV_TIMEOUT = 4,       // a bounded wait on a copy gave up
-    DEV_BAD_PAGE = 5,      // a position or page of a paged cache out of range
 };
 
 __device__ __forceinline__ void dev_error(uint32_t* status, uint32_t code, uint32_t detail)
@@ -349,27 +348,6 @@ struct PerKeyWs {
 int64_t per_key_groups(int64_t T_cap);
 cudaError_t set_per_key_wait_polls(int64_t polls);
 cudaError_t launch_per_key(const PerKeyArgs& a, const PerKeyWs& ws, cudaStream_t st);
-
-// Paged KV cache (k_paged_append.cu, k_paged_attn.cu).
-constexpr int SCALE_BLOCK = 16;   // tokens that share an e4m3 scale
-struct AppendArgs {
-    const __nv_bfloat16* k;
-    const __nv_bfloat16* v;
-    const __nv_bfloat16* q;      // nullable
-    __nv_bfloat16* q_out;
-    int64_t k_stride, v_stride, q_stride;
-    int64_t Nq;
-    int Hq;
-    const int32_t* start;
-    const int32_t* n_new;        // nullable
-    const float* inv_freq;
-    int rot;                     // rotated elements of a head
-    int interleaved;
-};
-cudaError_t launch_paged_append(const lsa_paged_kv& kv, const AppendArgs& a, cudaStream_t st);
-cudaError_t launch_paged_attn(const lsa_paged_kv& kv, const void* Q, int64_t Nq, int Hq,
-                              const int32_t* indices, const int32_t* counts, int s_max,
-                              float scale, void* O, float* lse, cudaStream_t st);
 
 // Checks run when LSA_DEBUG=1 (k_debug.cu).  Each synchronises the stream
 // (it does nothing while the stream is being captured) and returns in out[4]

@@ -1,12 +1,49 @@
-// paged.cuh -- device helpers of the paged KV cache's kernels.
+// paged.cuh -- declarations and device helpers of the paged KV cache (k_paged_append.cu,
+// k_paged_attn.cu).
 #pragma once
 
 #include "lsa_internal.cuh"
 
 namespace lsa {
 
+constexpr int SCALE_BLOCK = 16;   // tokens that share an e4m3 scale
+// status code beside those of DevErr: a position or page out of range
+constexpr uint32_t DEV_BAD_PAGE = 5;
+
+struct AppendArgs {
+    const __nv_bfloat16* k;
+    const __nv_bfloat16* v;
+    const __nv_bfloat16* q;      // nullable
+    __nv_bfloat16* q_out;
+    int64_t k_stride, v_stride, q_stride;
+    int64_t Nq;
+    int Hq;
+    const int32_t* start;
+    const int32_t* n_new;        // nullable
+    const float* inv_freq;
+    int rot;                     // rotated elements of a head
+    int interleaved;
+};
+cudaError_t launch_paged_append(const lsa_paged_kv& kv, const AppendArgs& a, cudaStream_t st);
+cudaError_t launch_paged_attn(const lsa_paged_kv& kv, const void* Q, int64_t Nq, int Hq,
+                              const int32_t* indices, const int32_t* counts, int s_max,
+                              float scale, void* O, float* lse, cudaStream_t st);
+
+// Waits until the kernels that this one was launched behind have ended and their
+// writes are visible.
+__device__ __forceinline__ void grid_dependency()
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+// Lets the kernel launched behind this one start as soon as every CTA of this one
+// has come here or ended.
+__device__ __forceinline__ void grid_release()
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // The kernel is set up while the one before it on the stream still runs and waits
-// for that one before it reads or writes anything (ptx::grid_dependency): calls in
+// for that one before it reads or writes anything (grid_dependency): calls in
 // a row are 1 to 2 us closer (8 tokens' append 5.1 us a call against 3.1, a 33-row
 // attention 10.2 against 8.1).  None lets a later call start before it ends: blocks
 // that wait on an SM leave the next grid unevenly spread (64 rows in bf16 pages

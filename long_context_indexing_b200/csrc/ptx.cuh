@@ -126,20 +126,6 @@ __device__ __forceinline__ void cp_async_wait()
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// ---- programmatic dependent launch ------------------------------------------
-// Waits until the kernels that this one was launched behind have ended and their
-// writes are visible.
-__device__ __forceinline__ void grid_dependency()
-{
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-// Lets the kernel launched behind this one start as soon as every CTA of this one
-// has come here or ended.
-__device__ __forceinline__ void grid_release()
-{
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
 // ---- warp-level MMA (bf16 in, fp32 accumulate) ----------------------------
 __device__ __forceinline__ void ldsm_x4(uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3,
                                         const void* p)

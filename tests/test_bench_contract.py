@@ -38,3 +38,12 @@ def test_warmup_below_three_is_refused():
                           "--workload", "tiny", "--warmup", "2"],
                          capture_output=True, text=True, timeout=120, cwd=ROOT)
     assert out.returncode != 0 and "warmup" in out.stderr
+
+
+def test_traffic_record_is_of_the_present_sources():
+    # the DRAM traffic that the bench line quotes was measured with the attention sources as
+    # they are: a change to one of them wants a new capture (or belongs in a file of its own)
+    sys.path.insert(0, ROOT)
+    import bench
+    rec = bench._traffic_record("prefill_attend_10m")
+    assert rec is not None and rec["dram_bytes_per_call"] > 0
