@@ -511,7 +511,9 @@ lsa_status lsa_prefill_chunk_host(lsa_index* idx, const void* h_latent_K, const 
  * Synchronous; applies to later launches on the current device. */
 lsa_status lsa_set_wait_limit(int64_t polls);
 
-/* Workspace bytes for lsa_decode_step (depends on the device's SM count). */
+/* Workspace bytes for lsa_decode_step (depends on the device's SM count); 0 on bad
+ * arguments, a selection of no key (budget + window + sinks = 0) among them, which
+ * the step refuses too. */
 size_t lsa_decode_workspace_bytes(const lsa_index* idx, int Hq, int Hkv, int d,
                                   lsa_select_params sp);
 

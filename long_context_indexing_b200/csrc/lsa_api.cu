@@ -151,6 +151,19 @@ lsa_status check_select(const lsa_index* idx, lsa_select_params sp, int s_max)
     return LSA_OK;
 }
 
+// A decode step's selection row of budget + window + sinks entries: at least one (the
+// layout divides by the row's length) and at most `most`.
+lsa_status check_step_row(lsa_select_params sp, int64_t most)
+{
+    if (sp.budget < 0 || sp.window < 0 || sp.sinks < 0)
+        return fail(LSA_ERR_INVALID_ARG, "budget/window/sinks must be >= 0");
+    const int64_t n = (int64_t)sp.budget + sp.window + sp.sinks;
+    if (n < 1 || n > most)
+        return fail(LSA_ERR_INVALID_ARG, "budget+window+sinks=%lld outside [1, %lld]",
+                    (long long)n, (long long)most);
+    return LSA_OK;
+}
+
 // The SIMT nominator keeps every eligible score in shared memory.
 constexpr int64_t SIMT_MAX_BUCKETS = (220 * 1024) / 4;
 
@@ -1142,7 +1155,7 @@ lsa_status lsa_set_wait_limit(int64_t polls)
 size_t lsa_decode_workspace_bytes(const lsa_index* idx, int Hq, int Hkv, int d,
                                   lsa_select_params sp)
 {
-    if (!idx || sp.budget < 0 || sp.window < 0 || sp.sinks < 0) return 0;
+    if (!idx || check_step_row(sp, INT32_MAX) != LSA_OK) return 0;
     if (check_attn_shape(Hq, Hkv, d, idx->v.dtype) != LSA_OK) return 0;
     return decode_layout(idx, Hq, Hkv, d, sp).total;
 }
@@ -1158,8 +1171,10 @@ lsa_status lsa_decode_step(lsa_index* idx, void* latent_K, void* K, void* V,
         !pos || !workspace || !O)
         return fail(LSA_ERR_INVALID_ARG, "NULL argument");
     const IndexView& v = idx->v;
+    lsa_status s = check_step_row(sp, INT32_MAX);
+    if (s != LSA_OK) return s;
     const int s_max = sp.budget + sp.window + sp.sinks;
-    lsa_status s = check_select(idx, sp, s_max);
+    s = check_select(idx, sp, s_max);
     if (s != LSA_OK) return s;
     s = check_attn_shape(Hq, Hkv, d, v.dtype);
     if (s != LSA_OK) return s;
@@ -1414,7 +1429,7 @@ PagedDecodeLayout paged_decode_layout(const lsa_index* idx, const lsa_paged_kv* 
 size_t lsa_decode_paged_workspace_bytes(const lsa_index* idx, const lsa_paged_kv* kv, int Hq,
                                         lsa_select_params sp)
 {
-    if (!idx || sp.budget < 0 || sp.window < 0 || sp.sinks < 0 || check_paged(kv) != LSA_OK ||
+    if (!idx || check_step_row(sp, INT32_MAX) != LSA_OK || check_paged(kv) != LSA_OK ||
         check_paged_heads(kv, Hq) != LSA_OK)
         return 0;
     return paged_decode_layout(idx, kv, Hq, sp).total;
@@ -1440,6 +1455,8 @@ lsa_status lsa_decode_step_paged(lsa_index* idx, const lsa_paged_kv* kv, void* l
     if (v.B != kv->B)
         return fail(LSA_ERR_INVALID_ARG, "the index holds %lld sequences, the cache %lld",
                     (long long)v.B, (long long)kv->B);
+    s = check_step_row(sp, INT32_MAX);
+    if (s != LSA_OK) return s;
     const int s_max = sp.budget + sp.window + sp.sinks;
     s = check_select(idx, sp, s_max);
     if (s != LSA_OK) return s;

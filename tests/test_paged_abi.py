@@ -118,6 +118,31 @@ def test_decode_step_arguments_refused():
     assert f(h, ctypes.byref(_kv()), 8, lsa.SelectParams(-1, 64, 4)) == 0
 
 
+def _sp(*a):
+    return lsa.SelectParams(*a)
+
+
+@pytest.mark.parametrize("sp", [(0, 0, 0), (2 ** 31 - 1, 1, 0), (2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1)])
+def test_decode_selections_without_a_key_or_past_int_refused(sp):
+    # an index of single keys (p = 1) lets the window be 0, so that nothing else refuses them
+    P = lsa.IndexParams(1, 256, 8, 3)
+    need = lsa._lib.lsa_index_bytes(2, 8192, P, lsa.BF16)
+    h = ctypes.c_void_p()
+    assert lsa._lib.lsa_index_init(ctypes.c_void_p(FAKE), need, 2, 8192, P, lsa.BF16,
+                                   ctypes.byref(h)) == 0
+    kv = ctypes.byref(_kv())
+    assert lsa._lib.lsa_decode_paged_workspace_bytes(h, kv, 8, _sp(*sp)) == 0
+    assert b"budget+window+sinks" in lsa._lib.lsa_last_error()
+    assert lsa._lib.lsa_decode_workspace_bytes(h, 8, 2, 128, _sp(*sp)) == 0
+    assert _step(h, sp=_sp(*sp)) == 1
+    assert b"budget+window+sinks" in lsa._lib.lsa_last_error()
+    assert lsa._lib.lsa_decode_step(h, *[FAKE] * 9, 8, 2, 128, _sp(*sp), FAKE, 1 << 40, FAKE, None) == 1
+    assert b"budget+window+sinks" in lsa._lib.lsa_last_error()
+    # one key is a selection
+    assert lsa._lib.lsa_decode_paged_workspace_bytes(h, kv, 8, _sp(0, 0, 1)) > 0
+    assert lsa._lib.lsa_decode_workspace_bytes(h, 8, 2, 128, _sp(0, 0, 1)) > 0
+
+
 def test_binding_is_built_for_this_torch_and_steps_aside():
     # wrong arguments of every kind come back as NotImplemented, for the Python path to name
     b = lsa._binding
