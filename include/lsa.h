@@ -622,8 +622,8 @@ lsa_status lsa_paged_append(const lsa_paged_kv* kv, const void* k, int64_t k_str
                             int interleaved, void* stream);
 
 /* lsa_sparse_attn over the paged cache: Q, O [B][Nq][Hq][d] bf16, indices
- * [B][Nq][s_max] positions (as the selections write them), counts [B][Nq].
- * fp32 softmax and accumulation; Hq a multiple of Hkv.  A row of count 0 gets
+ * [B][Nq][s_max] positions (as the selections write them; s_max up to 2^30),
+ * counts [B][Nq].  fp32 softmax and accumulation; Hq a multiple of Hkv.  A row of count 0 gets
  * O = 0 and lse = -inf; a listed position outside [0, max_pages * page), or
  * on a page outside [0, n_pages), is skipped and recorded in the status.  lse
  * (nullable) [B][Nq][Hq] f32: max + ln(sum) of the scaled logits.  For 8-bit

@@ -865,6 +865,8 @@ def lsa_paged_attn(cache, Q, indices, counts, scale=None, return_lse=False, out=
         raise ValueError("Q must be [%d][Nq][Hq][%d]" % (cache.B, cache.d))
     B, Nq, Hq, d = shape
     s_max = indices.shape[-1]
+    if s_max > 1 << 30:     # (past 32 bits ctypes would cut it short)
+        raise ValueError("rows of %d listed positions, more than 2^30" % s_max)
     _int32(cache, indices, "indices", (B, Nq, s_max))
     _int32(cache, counts, "counts", (B, Nq))
     if out is None:

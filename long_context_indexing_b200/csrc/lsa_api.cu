@@ -1272,6 +1272,10 @@ lsa_status lsa_select_noalloc(const lsa_index* idx, const void* latent_Q,
 // ---- paged KV cache -------------------------------------------------------------
 namespace {
 
+// Listed positions of a row at most: the attention's tiles look up to three steps past a
+// row's end (6,176 places) with 32-bit places.
+constexpr int PAGED_MAX_ROW = 1 << 30;
+
 lsa_status check_paged(const lsa_paged_kv* kv)
 {
     if (!kv) return fail(LSA_ERR_INVALID_ARG, "NULL cache");
@@ -1388,6 +1392,8 @@ lsa_status lsa_paged_attn(const lsa_paged_kv* kv, const void* Q, int64_t Nq, int
     if (s != LSA_OK) return s;
     if (!Q || !indices || !counts || !O) return fail(LSA_ERR_INVALID_ARG, "NULL argument");
     if (Nq < 0 || s_max < 1) return fail(LSA_ERR_INVALID_ARG, "bad sizes");
+    if (s_max > PAGED_MAX_ROW)
+        return fail(LSA_ERR_UNSUPPORTED, "s_max=%d > %d", s_max, PAGED_MAX_ROW);
     s = check_paged_heads(kv, Hq);
     if (s != LSA_OK) return s;
     if (Nq > 2147483647LL / (kv->B * Hq))
@@ -1429,7 +1435,7 @@ PagedDecodeLayout paged_decode_layout(const lsa_index* idx, const lsa_paged_kv* 
 size_t lsa_decode_paged_workspace_bytes(const lsa_index* idx, const lsa_paged_kv* kv, int Hq,
                                         lsa_select_params sp)
 {
-    if (!idx || check_step_row(sp, INT32_MAX) != LSA_OK || check_paged(kv) != LSA_OK ||
+    if (!idx || check_step_row(sp, PAGED_MAX_ROW) != LSA_OK || check_paged(kv) != LSA_OK ||
         check_paged_heads(kv, Hq) != LSA_OK)
         return 0;
     return paged_decode_layout(idx, kv, Hq, sp).total;
@@ -1455,7 +1461,7 @@ lsa_status lsa_decode_step_paged(lsa_index* idx, const lsa_paged_kv* kv, void* l
     if (v.B != kv->B)
         return fail(LSA_ERR_INVALID_ARG, "the index holds %lld sequences, the cache %lld",
                     (long long)v.B, (long long)kv->B);
-    s = check_step_row(sp, INT32_MAX);
+    s = check_step_row(sp, PAGED_MAX_ROW);
     if (s != LSA_OK) return s;
     const int s_max = sp.budget + sp.window + sp.sinks;
     s = check_select(idx, sp, s_max);

@@ -118,6 +118,33 @@ def test_decode_step_arguments_refused():
     assert f(h, ctypes.byref(_kv()), 8, lsa.SelectParams(-1, 64, 4)) == 0
 
 
+@pytest.mark.parametrize("s_max,code", [(1 << 30, 0), ((1 << 30) + 1, 7), (2 ** 31 - 1, 7)])
+def test_rows_whose_tiles_would_pass_32_bits_refused(s_max, code):
+    # a tile's places and three steps of 64 tiles of 32 past the row's end must fit 32 bits
+    assert (1 << 30) + 4 * 64 * 32 < 2 ** 31
+    assert _attn(Nq=0, s_max=s_max) == code          # (no launch either way)
+    h = _index()
+    f = lsa._lib.lsa_decode_paged_workspace_bytes
+    n = f(h, ctypes.byref(_kv()), 8, lsa.SelectParams(s_max - 68, 64, 4))
+    assert (n > 0) == (code == 0)
+    assert _step(h, sp=lsa.SelectParams(s_max - 68, 64, 4)) == 1
+    assert (b"budget+window+sinks" in lsa._lib.lsa_last_error()) == (code != 0)
+
+
+def test_python_refuses_rows_past_32_bits():
+    # a row of 2^32 + 5 positions must not reach the library as one of 5
+    import types
+    cache = types.SimpleNamespace(B=1, d=64, _index=-1, device=torch.device("cpu"), _addr=0, _ref=None)
+    Q = torch.zeros(1, 1, 2, 64, dtype=torch.bfloat16)
+    idx = torch.zeros(1, dtype=torch.int32).expand(1, 1, 2 ** 32 + 5)
+    cnt = torch.zeros(1, 1, dtype=torch.int32)
+    with pytest.MonkeyPatch.context() as m:
+        m.setattr(lsa, "_binding", None)
+        m.setattr(lsa, "_current_device", lambda: -1)
+        with pytest.raises(ValueError, match="2\\^30"):
+            lsa.lsa_paged_attn(cache, Q, idx, cnt)
+
+
 def _sp(*a):
     return lsa.SelectParams(*a)
 
