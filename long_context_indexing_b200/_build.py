@@ -6,7 +6,9 @@ driver at run time (the runtime is linked statically), so loading it on a
 host without a GPU succeeds; the first CUDA call then fails cleanly.
 
 csrc/py/paged_binding.cpp, the binding of the paged cache's per-token calls, is
-compiled against the installed torch and Python into _paged_binding.so beside it.
+compiled against the installed torch and Python into _paged_binding with Python's own
+suffix beside it.  It is optional: without torch or a C++ compiler that takes it, the
+library is built all the same and those calls go through ctypes.
 """
 import concurrent.futures as cf
 import glob
@@ -24,7 +26,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "liblsa.so")
 BINDING_SRC = os.path.join(CSRC, "py", "paged_binding.cpp")
-BINDING = os.path.join(PKG, "_paged_binding.so")
+BINDING = os.path.join(PKG, "_paged_binding" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 CXX = os.environ.get("CXX", "g++")
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
@@ -62,7 +64,10 @@ def _compile(src, verbose_ptxas=False):
 
 
 def _build_binding(force=False):
-    torch_dir = importlib.util.find_spec("torch").submodule_search_locations[0]
+    torch = importlib.util.find_spec("torch")
+    if torch is None:
+        raise RuntimeError("no torch")
+    torch_dir = torch.submodule_search_locations[0]
     version_py = os.path.join(torch_dir, "version.py")
     if not force and not _stale(BINDING, [BINDING_SRC, version_py, *_headers()]):
         return
@@ -78,8 +83,23 @@ def _build_binding(force=False):
            "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError("binding failed:\n%s%s" % (r.stdout, r.stderr))
+        raise RuntimeError("%s failed:\n%s%s" % (CXX, r.stdout, r.stderr))
     os.replace(tmp, BINDING)
+
+
+def _finish_binding(result):
+    """Takes the outcome of _build_binding: where it failed there is no binding, not an old one."""
+    any_python = os.path.join(os.path.dirname(BINDING), "_paged_binding.so")
+    gone = [any_python] if any_python != BINDING else []
+    try:
+        result()
+    except Exception as e:
+        sys.stderr.write("warning: no compiled binding of the paged cache's calls (they go through "
+                         "ctypes): %s\n" % e)
+        gone.append(BINDING)
+    for path in gone:
+        if os.path.exists(path):
+            os.remove(path)
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
@@ -94,7 +114,6 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
         binding = ex.submit(_build_binding, force)
         results = list(ex.map(lambda s: _compile(s, verbose_ptxas), srcs))
-        binding.result()
     objs = [o for o, _ in results]
     if verbose_ptxas:
         for (_, log), s in zip(results, srcs):
@@ -107,6 +126,7 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError("link failed:\n%s%s" % (r.stdout, r.stderr))
         os.replace(tmp, LIB)
+    _finish_binding(binding.result)
     return LIB
 
 
