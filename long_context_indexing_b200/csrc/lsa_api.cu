@@ -1539,9 +1539,6 @@ lsa_status lsa_paged_check(const lsa_paged_kv* kv, void* stream)
     if (e != cudaSuccess) return cuda_fail(e, "cache check");
     switch (h[0]) {
     case DEV_OK: return LSA_OK;
-    case DEV_BAD_INDEX:
-        return fail(LSA_ERR_INVALID_ARG, "a listed position (%d) was outside the page table",
-                    (int)h[2]);
     case DEV_BAD_PAGE:
         return fail(LSA_ERR_INVALID_ARG,
                     "a position (%d) outside the page table, or on a page outside the pool",

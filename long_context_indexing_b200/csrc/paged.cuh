@@ -57,19 +57,6 @@ inline cudaLaunchAttribute dependent_launch()
     return at;
 }
 
-// The page that holds position t of sequence b, or -1 (recorded) when the
-// position is outside the table or the page outside the pool.
-__device__ __forceinline__ int32_t page_of(const lsa_paged_kv& kv, int64_t b, int64_t t)
-{
-    int32_t pg = -1;
-    if (t >= 0 && t < kv.max_pages * kv.page) {
-        pg = kv.page_table[b * kv.max_pages + t / kv.page];
-        if (pg < 0 || pg >= kv.n_pages) pg = -1;
-    }
-    if (pg < 0) dev_error(kv.status, DEV_BAD_PAGE, (uint32_t)t);
-    return pg;
-}
-
 // Smallest power of two 2^k, k >= -64, with amax <= 448 * 2^k (448 = 0.875 * 2^9).
 __device__ __forceinline__ float e4m3_scale(float amax)
 {
