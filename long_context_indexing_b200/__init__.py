@@ -908,6 +908,7 @@ def lsa_decode_step_paged(index, cache, latent_K, new_latent_k, new_k, new_v, la
             return lsa_decode_step_paged(index, cache, latent_K, new_latent_k, new_k, new_v,
                                          latent_q, q, pos, budget, window, sinks, inv_freq,
                                          interleaved, workspace, out)
+    _same_device(cache.device, index.buffer)
     B, Hkv, d = cache.B, cache.Hkv, cache.d
     Hq = q.shape[1]
     _like(cache, latent_K, "latent_K", (index.B, index.T_cap, 64))

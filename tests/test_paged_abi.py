@@ -193,6 +193,19 @@ def test_handle_wants_cuda_tensors_of_one_kind():
         lsa.LsaPagedKV(k, k, torch.zeros(1, 4, dtype=torch.int32))
 
 
+def test_decode_step_wants_the_index_on_the_caches_device():
+    # the kernels would read the index's memory from another GPU
+    import types
+    cache = types.SimpleNamespace(B=1, Hkv=2, d=64, _index=0, device=torch.device("cuda", 0))
+    index = types.SimpleNamespace(B=1, T_cap=64, buffer=types.SimpleNamespace(
+        device=torch.device("cuda", 1)))
+    t = torch.zeros(1, 2, 64, dtype=torch.bfloat16)
+    with pytest.MonkeyPatch.context() as m:
+        m.setattr(lsa, "_current_device", lambda: 0)
+        with pytest.raises(ValueError, match="different devices"):
+            lsa.lsa_decode_step_paged(index, cache, t, t, t, t, t, t, t, 1, 1, 1)
+
+
 def test_plain_grid_is_torchs_e4m3():
     rng = np.random.default_rng(0)
     x = np.concatenate([rng.standard_normal(20000) * np.exp2(rng.uniform(-14, 9, 20000)),
