@@ -612,7 +612,8 @@ typedef struct {
  * mean nothing until a token is appended there.
  * A token whose page is not in [0, n_pages) or whose position is outside
  * [0, max_pages * page) is left out of the cache and recorded in the status;
- * a negative start leaves out the whole sequence.  A page that receives tokens
+ * a negative start leaves out the whole sequence, whose rows of q_out become
+ * zeros (unless q_out == q: then they stay).  A page that receives tokens
  * must belong to one sequence of the call.  Asynchronous on `stream`,
  * graph-capturable, no workspace. */
 lsa_status lsa_paged_append(const lsa_paged_kv* kv, const void* k, int64_t k_stride,

@@ -805,7 +805,7 @@ def lsa_paged_append(cache, k, v, start, n_new=None, q=None, q_out=None, inv_fre
     start[b] + i of the paged cache, keys rotated by inv_freq [rot_dim / 2] float32 (None: no
     rotation); tokens at and after n_new[b] are padding.  With q [B][Nq][Hq][d] the queries are
     rotated too: into q_out (which may be q; rows of padding are left as they are) or a new
-    tensor, which is returned (None without q).  C: lsa_paged_append."""
+    tensor (rows of padding are zeros), which is returned (None without q).  C: lsa_paged_append."""
     if stream is None and _binding is not None:
         r = _binding.append(cache._addr, cache._index, k, v, start, n_new, q, q_out, inv_freq,
                             interleaved)
@@ -829,7 +829,9 @@ def lsa_paged_append(cache, k, v, start, n_new=None, q=None, q_out=None, inv_fre
     if q is not None:
         qs, Hq = _rows(cache, q, "q", B, Nq, None), q.shape[2]
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=cache.device)
+            # (the call leaves the rows of padding as they are)
+            q_out = (torch.empty if n_new is None else torch.zeros)(
+                q.shape, dtype=torch.bfloat16, device=cache.device)
         else:
             _like(cache, q_out, "q_out", q.shape)
     elif q_out is not None:

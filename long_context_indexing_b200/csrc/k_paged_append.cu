@@ -154,9 +154,16 @@ __global__ void __launch_bounds__(PA_THREADS, 3) paged_append_kernel(lsa_paged_k
     int64_t n = a.n_new ? a.n_new[b] : a.Nq;
     if (n > a.Nq) n = a.Nq;
     if (n <= 0) return;
-    if (start < 0) {
+    if (start < 0) {                         // left out: queries of zeros, unless in place
         if (blockIdx.x == 0 && threadIdx.x == 0 && do_kv)
             dev_error(kv.status, DEV_BAD_PAGE, (uint32_t)start);
+        if (do_q && a.q_out != a.q) {
+            const int64_t part = gridDim.z > 2 ? (int)blockIdx.z - 1 : 0;
+            uint4* dst = reinterpret_cast<uint4*>(a.q_out + b * a.Nq * a.Hq * D);
+            for (int64_t i = (blockIdx.x * parts + part) * PA_THREADS + threadIdx.x;
+                 i < n * a.Hq * (D / 8); i += (int64_t)gridDim.x * parts * PA_THREADS)
+                dst[i] = make_uint4(0u, 0u, 0u, 0u);
+        }
         return;
     }
     const int64_t p0 = (start / SCALE_BLOCK + blockIdx.x) * SCALE_BLOCK;

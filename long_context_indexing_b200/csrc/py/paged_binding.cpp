@@ -91,7 +91,9 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n)
             if (qs < 0) NO;
             Hq = q->size(2);
             if (a[7] == Py_None) {
-                made = at::empty(q->sizes(), q->options(), at::MemoryFormat::Contiguous);
+                // (the call leaves the rows of padding as they are)
+                made = n_new ? at::zeros(q->sizes(), q->options())
+                             : at::empty(q->sizes(), q->options(), at::MemoryFormat::Contiguous);
                 q_out = &made;
             } else if (!flat(q_out = tensor(a[7]), dev, at::kBFloat16, q->sizes())) {
                 NO;
