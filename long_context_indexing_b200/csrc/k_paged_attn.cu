@@ -206,7 +206,7 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
     const int nh = min(PT_H, a.hpg - h0);
     const int64_t hbase = row * a.Hq + (int64_t)g * a.hpg + h0;
     const int64_t b = row / a.Nq;
-    const int n = min(max(__ldg(a.counts + row), 0), a.s_max);
+    const int n = min(max(a.counts[row], 0), a.s_max);
     const int32_t* idx = a.indices + row * a.s_max;
     const int32_t* table = kv.page_table + b * kv.max_pages;
     const uint32_t t_end = (uint32_t)(kv.max_pages << a.page_shift);
@@ -279,7 +279,7 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
     for (int s = 0; s < C::KS; ++s) {
         const int c = E4M3 ? (s / 4) * 64 + t4 * 16 + (s % 4) * 4 : (s / 2) * 32 + t4 * 8 + (s % 2) * 4;
         qw[s] = make_uint2(0u, 0u);
-        if (r8 < nh) qw[s] = __ldg(reinterpret_cast<const uint2*>(a.Q + (hbase + r8) * D + c));
+        if (r8 < nh) qw[s] = *reinterpret_cast<const uint2*>(a.Q + (hbase + r8) * D + c);
     }
 
     // the first tile: in the loop, slot and slot1 are the tile's and the next
@@ -287,9 +287,9 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
     // asked for
     int32_t slot = -1, slot1 = -1;
     if (tile < n_tiles) {
-        const int32_t p0 = __ldg(position(tile)), p1 = __ldg(position(tile + step));
+        const int32_t p0 = *position(tile), p1 = *position(tile + step);
         copy4(pos_s, position(tile + 2 * step));
-        const int32_t g0 = __ldg(page(p0)), g1 = __ldg(page(p1));
+        const int32_t g0 = *page(p0), g1 = *page(p1);
         slot = slot_of(p0, g0, tile);
         copy_scales(0, slot);
         copy_k(1, slot, 0, some);

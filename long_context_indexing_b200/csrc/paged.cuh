@@ -30,7 +30,10 @@ cudaError_t launch_paged_attn(const lsa_paged_kv& kv, const void* Q, int64_t Nq,
                               float scale, void* O, float* lse, cudaStream_t st);
 
 // Waits until the kernels that this one was launched behind have ended and their
-// writes are visible.
+// writes are visible.  What they may have written is read after it by ordinary loads and
+// asynchronous copies only: a load through the read-only path (__ldg) says that its data
+// does not change while the kernel lives, which it may before this wait, and the compiler
+// may move such a load ahead of it.
 __device__ __forceinline__ void grid_dependency()
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");

@@ -239,3 +239,16 @@ def test_plain_append_and_attend_on_a_worked_case():
     Kv = st["K"] * st["scales"][0, 0, 0, 0]
     O, _, _, lse = plain.attend(Kv, Kv, st["table"], 2 * one, np.array([[[1, 0]]]), np.array([[1]]), 1.0)
     assert O[0, 0, 0, 0] == 7.0 and lse[0, 0, 0] == 49.0
+
+
+def test_dependent_kernels_read_nothing_as_unchanging():
+    # these kernels start while the one before them still writes what they will read: no load
+    # of theirs may go through the read-only path, and their pointers promise nothing that lets
+    # the compiler choose it
+    import os
+    import re
+    src = os.path.join(os.path.dirname(lsa.__file__), "csrc")
+    for name in ("k_paged_append.cu", "k_paged_attn.cu", "paged.cuh"):
+        with open(os.path.join(src, name)) as f:
+            code = re.sub(r"//[^\n]*", "", f.read())
+        assert not re.search(r"__ldg|\.global\.nc|__restrict__|__ldlu", code), name
