@@ -101,7 +101,6 @@ struct PagedAttnArgs {
     int page_shift;
     float scale_log2;                // scale * log2(e)
     int64_t unit0;                   // this launch's first unit
-    bool leads, follows;             // the first, the second launch of a call with two
     __nv_bfloat16* O;
     float* lse;
 };
@@ -189,11 +188,7 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
     uint32_t rank, n_cta;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(n_cta));
-    // A second launch starts as the first one's CTAs end: those have waited for all that
-    // came before, and it waits for them before it ends, so that whoever waits for the
-    // second has waited for both.
-    if (!a.follows) grid_dependency();
-    if (a.leads) grid_release();
+    grid_dependency();
     // the CTAs of the cluster have started before any is written to
     if (n_cta > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -595,7 +590,6 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
             if (a.lse && dim == 0)
                 a.lse[hbase + h] = L == 0.f ? -INFINITY : (M1 + log2f(L)) * 0.6931471805599453f;
         }
-        if (a.follows) grid_dependency();
         return;
     }
     // this CTA finishes the elements of threads rank * tpc .. of every CTA
@@ -624,7 +618,6 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
                 a.lse[hbase + hh] = S == 0.f ? -INFINITY : (N1 + log2f(S)) * 0.6931471805599453f;
         }
     }
-    if (a.follows) grid_dependency();
 }
 
 cudaError_t launch_paged_attn(const lsa_paged_kv& kv, const void* Q, int64_t Nq, int Hq,
@@ -675,15 +668,17 @@ cudaError_t launch_paged_attn(const lsa_paged_kv& kv, const void* Q, int64_t Nq,
     };
     // Units past the last whole wave would run alone for as long as a full wave's.  Where
     // they fill less than 3/8 of one they follow in a launch of their own, split like a
-    // small call's, that starts on the places that the first launch leaves (502 bf16
-    // units of 4,612 keys: 129 us in one launch, 108 in two; 640 8-bit units of 2,564
-    // keys 85.6 against 71; 1,240 units 140 against 129).  With more of them there is
-    // little to win (700 bf16 units 149.5 against 154), nor with short rows (596 units of
-    // 260 keys 15.5 against 17.2; of 1,156 keys 37.8 against 32.2) or after many waves
-    // (6,000 units 602 either way).  Rows of unequal length fill the last wave by
-    // themselves and lose by it (640 units of 0 to 2,564 keys 42.1 against 44.8), but
-    // only the device knows their counts.
-    const int64_t rest = units > slots && units < 8 * slots && s_max >= 1024 ? units % slots : 0;
+    // small call's (502 bf16 units of 4,612 keys: 117 us in one launch, 101 in two; 446 of
+    // them 114 against 91; 950 of them 191 against 178; 640 8-bit units of 2,564 keys 85
+    // against 75, of 4,612 keys 145 against 122).  With more of them there is little to win
+    // (700 bf16 units 149.5 against 154), nor with short rows (596 units of 260 keys 15.5
+    // against 17.2; of 1,156 keys 41.0 against 40.7) or after three waves (1,840 units 183
+    // against 184).  The second launch waits for the first one's end before it reads, as
+    // everything that may read what an earlier kernel wrote: with rows of unequal length,
+    // which fill the last wave by themselves, that wait is lost (640 units of 0 to 2,564
+    // keys 42 us in one launch, 52 in two; 502 bf16 units of 0 to 4,612 keys 63 against
+    // 76), but only the device knows their counts.
+    const int64_t rest = units > slots && units < 3 * slots && s_max >= 1024 ? units % slots : 0;
     const int64_t behind = rest <= slots * 3 / 8 ? rest : 0;
     auto run = [&](auto kern, int bytes) {
         cudaError_t e = ensure_smem_attr((const void*)kern, bytes);
@@ -711,13 +706,9 @@ cudaError_t launch_paged_attn(const lsa_paged_kv& kv, const void* Q, int64_t Nq,
             return e;
         };
         a.unit0 = 0;
-        a.leads = behind > 0;
-        a.follows = false;
         e = launch(units - behind);
         if (e != cudaSuccess || behind == 0) return e;
         a.unit0 = units - behind;
-        a.leads = false;
-        a.follows = true;
         return launch(behind);
     };
     cudaError_t e;

@@ -38,20 +38,13 @@ __device__ __forceinline__ void grid_dependency()
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }
-// Lets the kernel launched behind this one start as soon as every CTA of this one
-// has come here or ended.
-__device__ __forceinline__ void grid_release()
-{
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
 
 // The kernel is set up while the one before it on the stream still runs and waits
 // for that one before it reads or writes anything (grid_dependency): calls in
 // a row are 1 to 2 us closer (8 tokens' append 5.1 us a call against 3.1, a 33-row
 // attention 10.2 against 8.1).  None lets a later call start before it ends: blocks
 // that wait on an SM leave the next grid unevenly spread (64 rows in bf16 pages
-// 52.0 us against 56.6 and more); only the second launch of one attention call
-// starts on the places that the first one leaves.
+// 52.0 us against 56.6 and more).
 inline cudaLaunchAttribute dependent_launch()
 {
     cudaLaunchAttribute at;

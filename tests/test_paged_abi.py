@@ -252,3 +252,23 @@ def test_dependent_kernels_read_nothing_as_unchanging():
         with open(os.path.join(src, name)) as f:
             code = re.sub(r"//[^\n]*", "", f.read())
         assert not re.search(r"__ldg|\.global\.nc|__restrict__|__ldlu", code), name
+
+
+def test_dependent_kernels_wait_before_they_read():
+    # every kernel that may start before its predecessor has ended waits for it in its first
+    # statements, on every path and in every launch of a call, and none lets a later one start
+    # early: what a kernel may see of earlier writes is promised after its own wait only
+    import os
+    import re
+    src = os.path.join(os.path.dirname(lsa.__file__), "csrc")
+    for name in ("k_paged_append.cu", "k_paged_attn.cu"):
+        with open(os.path.join(src, name)) as f:
+            code = re.sub(r"//[^\n]*", "", f.read())
+        assert "launch_dependents" not in code and "grid_release" not in code, name
+        kernels = code.split("__global__")[1:]
+        assert kernels
+        for k in kernels:
+            head = k[k.index("{"):k.index("grid_dependency();")]
+            assert k.count("grid_dependency();") == 1, name
+            # declarations and special registers only: no branch, no access to memory
+            assert not re.search(r"\bif\b|\bfor\b|->|\ba\.|\bkv\.", head), (name, head)
