@@ -62,7 +62,8 @@ constexpr int PT_WARPS = 4;
 constexpr int PT_THREADS = 32 * PT_WARPS;
 constexpr int PT_H = 8;             // query heads of a unit
 constexpr int PT_MAX_C = 16;        // CTAs of a cluster at most
-constexpr float PT_NONE = -3e38f;   // reference before any key
+constexpr float PT_NONE = -3e38f;   // reference before any key's logit
+constexpr float PT_EMPTY = -3.4e38f;   // the reference that a warp without a key hands on
 constexpr float PT_SLACK = 15.f;    // log2 that a value may pass the reference by
 constexpr float PT_UP = 7.f;        // log2 of the f16 weight at its reference's maximum
 
@@ -333,6 +334,7 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
     float m1[2] = {PT_NONE, PT_NONE}, m2[2] = {PT_NONE, PT_NONE}, l[2] = {0.f, 0.f};
+    bool met = false;                                   // a key with a slot
     // this lane's offsets inside a stage: K rows r8, r8 + 8; V rows 2 t4 ...
     const int k_at = (r8 * C::ROWB + t4 * 16) ^ (C::ROWB >= 128 ? (r8 & 1) << 6 : 0);
     const int v_at = C::HALF + ((2 * t4 * C::ROWB + r8 * (E4M3 ? D / 8 : 16)) ^ (t4 << 5));
@@ -372,6 +374,7 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
 
     for (int it = 0; tile < n_tiles; tile += step, ++it) {
         const uint32_t valid = __ballot_sync(0xffffffffu, slot >= 0);
+        met |= valid != 0u;
         // every row that this tile copies has a slot
         const bool whole = __all_sync(0xffffffffu, slot1 >= 0) && valid == 0xffffffffu;
 #pragma unroll
@@ -411,8 +414,15 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
             if (valid != 0xffffffffu) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (!(valid >> (half * 16 + (i >> 1) * 8 + r8) & 1)) d1[i] = d2[i] = -INFINITY;
+                    if (!(valid >> (half * 16 + (i >> 1) * 8 + r8) & 1)) {
+                        d1[i] = d2[i] = -INFINITY;
+                        z[i] = 0.f;                     // (NaN where Q is not finite)
+                    }
             }
+            // a key's product of -inf has the weight 0 of no key: infinities and NaN of Q
+            // or K reach the sum by themselves
+#pragma unroll
+            for (int i = 0; i < 4; ++i) l[i & 1] = fmaf(z[i], 0.f, l[i & 1]);
             float top = fmaxf(fmaxf(d1[0], d1[1]), fmaxf(d1[2], d1[3]));
             if (E4M3) top = fmaxf(top, fmaxf(fmaxf(d2[0], d2[1]), fmaxf(d2[2], d2[3])));
             if (__any_sync(0xffffffffu, top > PT_SLACK)) {
@@ -524,7 +534,7 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
         for (int o = 4; o <= 16; o <<= 1) l[c] += __shfl_xor_sync(0xffffffffu, l[c], o);
         if (r8 == 0) {
             float* ml = ml_s + warp * 3 * PT_H + 2 * t4 + c;
-            ml[0] = m1[c];
+            ml[0] = met ? m1[c] : PT_EMPTY;
             ml[PT_H] = E4M3 ? m2[c] : m1[c];
             ml[2 * PT_H] = l[c];
         }
@@ -545,7 +555,7 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
     const int dr = combo & 7;
     const int dim = E4M3 ? dr * (D / 8) + part * C::EPT
                          : (C::EPT == 8 ? part * 64 + dr * 8 : dr * 8 + part * 4);
-    float M1 = PT_NONE, M2 = PT_NONE, L = 0.f, o[C::EPT];
+    float M1 = PT_EMPTY, M2 = PT_NONE, L = 0.f, o[C::EPT];
 #pragma unroll
     for (int w = 0; w < PT_WARPS; ++w) {
         M1 = fmaxf(M1, ml_s[w * 3 * PT_H + h]);
@@ -578,17 +588,18 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
                      ::: "memory");
     }
     if (n_cta == 1) {
-        const float f = L == 0.f ? 0.f : ex2(M2 - M1) / L;
+        const bool empty = M1 == PT_EMPTY;
+        const float f = ex2(M2 - M1) / L;
         if (h < nh) {
             __nv_bfloat16* dst = a.O + (hbase + h) * D + dim;
             uint32_t w[C::EPT / 2];
 #pragma unroll
             for (int i = 0; i < C::EPT / 2; ++i)
-                w[i] = ptx::pack_bf16(L == 0.f ? 0.f : o[2 * i] * f, L == 0.f ? 0.f : o[2 * i + 1] * f);
+                w[i] = ptx::pack_bf16(empty ? 0.f : o[2 * i] * f, empty ? 0.f : o[2 * i + 1] * f);
             if (C::EPT == 8) *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
             else *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
             if (a.lse && dim == 0)
-                a.lse[hbase + h] = L == 0.f ? -INFINITY : (M1 + log2f(L)) * 0.6931471805599453f;
+                a.lse[hbase + h] = empty ? -INFINITY : (M1 + log2f(L)) * 0.6931471805599453f;
         }
         return;
     }
@@ -600,7 +611,7 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
         const int cb = t & 63, pt = t >> 6, hh = 2 * (cb >> 3 & 3) + (cb >> 5), rr = cb & 7;
         const int dd = (E4M3 ? rr * (D / 8) + pt * C::EPT
                              : (C::EPT == 8 ? pt * 64 + rr * 8 : rr * 8 + pt * 4)) + i;
-        float N1 = PT_NONE, N2 = PT_NONE, S = 0.f, v = 0.f;
+        float N1 = PT_EMPTY, N2 = PT_NONE, S = 0.f, v = 0.f;
 #pragma unroll 4
         for (uint32_t c = 0; c < n_cta; ++c) {
             N1 = fmaxf(N1, recv_ml[c * 3 * PT_H + hh]);
@@ -613,9 +624,10 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
             v += recv[c * tpc * C::EPT + x] * ex2(ml[PT_H] - N2);
         }
         if (hh < nh) {
-            a.O[(hbase + hh) * D + dd] = __float2bfloat16_rn(S == 0.f ? 0.f : v * (ex2(N2 - N1) / S));
+            const bool empty = N1 == PT_EMPTY;
+            a.O[(hbase + hh) * D + dd] = __float2bfloat16_rn(empty ? 0.f : v * (ex2(N2 - N1) / S));
             if (a.lse && dd == 0)
-                a.lse[hbase + hh] = S == 0.f ? -INFINITY : (N1 + log2f(S)) * 0.6931471805599453f;
+                a.lse[hbase + hh] = empty ? -INFINITY : (N1 + log2f(S)) * 0.6931471805599453f;
         }
     }
 }

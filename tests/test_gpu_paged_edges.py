@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import paged_plain as plain
-from test_gpu_paged import FP8, _cache, _check_append, _check_attn, _freq, _new, _rows, _state, lsa
+from test_gpu_paged import FP8, _cache, _check_attn, _freq, _new, _rows, _state, lsa
 
 pytestmark = pytest.mark.gpu
 
@@ -53,3 +53,136 @@ def test_append_leaves_no_row_of_a_new_tensor_unwritten(compiled, B, Nq, Hq, mon
     assert torch.equal(mine[3:], want[3:])
     with pytest.raises(lsa.LsaError):
         c.check()                                        # the negative start
+
+
+# few units (clusters of several CTAs), many (a CTA each), more than one launch
+SPLITS = [(1, 3, 700), (1, 420, 60), (1, 300, 1100)]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, FP8])
+@pytest.mark.parametrize("B,Nq,s", SPLITS)
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_attention_with_a_query_that_is_not_finite(dtype, B, Nq, s, bad):
+    # every logit of that head is an infinity or NaN, all of them -inf for some: its results are
+    # NaN, never those of an empty row; other heads and rows do not notice, and a row without a
+    # key stays empty
+    rng = np.random.default_rng(101)
+    Hq, Hkv, d, page, mp = 8, 2, 64, 16, 30
+    c = _cache(rng, B, Hkv, d, page, mp, dtype)
+    if dtype == FP8:
+        c.k_pages.view(torch.uint8).bitwise_and_(0x7F)  # (no key's sign differs)
+    else:
+        c.k_pages.abs_()
+    idx, cnt = _rows(rng, B, Nq, mp * page, s, [s, 1, s, 0, 17])
+    cnt[0, 2] = 5
+    idx[0, 2, :5] = -1                                  # only positions that are skipped
+    Q = _new(rng, B, Nq, Hq, d)
+    Q[:, :, 3] = Q[:, :, 3].abs()                       # one head: all logits of one sign
+    Q[:, :, 3, 7], Q[:, :, 6, 50] = bad, bad
+    O, l = lsa.lsa_paged_attn(c, Q.cuda(), torch.from_numpy(idx).cuda(), torch.from_numpy(cnt).cuda(),
+                              return_lse=True)
+    with pytest.raises(lsa.LsaError):
+        c.check()                                       # the skipped positions
+    full = torch.from_numpy(cnt > 0)
+    full[0, 2] = False
+    for h in (3, 6):
+        assert torch.isnan(O[:, :, h].cpu()[full]).all() and torch.isnan(l[:, :, h].cpu()[full]).all()
+    empty = ~full
+    assert (O.cpu()[empty] == 0).all() and torch.isneginf(l.cpu()[empty]).all()
+    fine = [0, 1, 2, 4, 5, 7]                           # (three of each KV head's four)
+    some = np.arange(min(Nq, 12))
+    _check_attn(c, Q[:, some][:, :, fine], idx[:, some], cnt[:, some], 1 / np.sqrt(d),
+                O[:, some][:, :, fine], l[:, some][:, :, fine])
+
+
+@pytest.mark.parametrize("dtype,bad", [(torch.bfloat16, float("inf")), (torch.bfloat16, float("-inf")),
+                                       (torch.bfloat16, float("nan")), (FP8, float("nan"))])
+@pytest.mark.parametrize("B,Nq,s", SPLITS)
+@pytest.mark.parametrize("which", ["K", "V"])
+def test_attention_over_a_listed_row_that_is_not_finite(dtype, bad, B, Nq, s, which):
+    # a key's element: every head of its KV head is NaN in the rows that list it, whatever the
+    # sign of the product; a value's element: that element is, and lse is not; rows that do not
+    # list it, the other KV head and the other elements do not notice
+    rng = np.random.default_rng(103)
+    Hq, Hkv, d, page, mp = 8, 2, 128, 16, 30
+    c = _cache(rng, B, Hkv, d, page, mp, dtype)
+    clean = _state(c)
+    idx, cnt = _rows(rng, B, Nq, mp * page - 1, s, [s, 1, s, 0, 17])    # (the last position in none)
+    T = mp * page - 1
+    hit = np.zeros((B, Nq), bool)
+    for b in range(B):
+        for i in range(0, Nq, 3):
+            if cnt[b, i] > 0:
+                idx[b, i, rng.integers(cnt[b, i])] = T
+                hit[b, i] = True
+    pages = c.k_pages if which == "K" else c.v_pages
+    for b in range(B):
+        pg = c.page_table[b, T // page]
+        if dtype == FP8:
+            pages.view(torch.uint8)[pg, T % page, 1, 9] = 0x7F
+        else:
+            pages[pg, T % page, 1, 9] = bad
+    Q = _new(rng, B, Nq, Hq, d)
+    O, l = lsa.lsa_paged_attn(c, Q.cuda(), torch.from_numpy(idx).cuda(), torch.from_numpy(cnt).cuda(),
+                              return_lse=True)
+    c.check()
+    O, l, hit = O.cpu(), l.cpu(), torch.from_numpy(hit)
+    assert hit.any() and (~hit).any()
+    if which == "K":
+        assert torch.isnan(O[:, :, 4:][hit]).all() and torch.isnan(l[:, :, 4:][hit]).all()
+    else:
+        assert (~torch.isfinite(O[:, :, 4:, 9][hit])).all()
+    # against the clean cache everywhere else
+    st = dict(clean)
+    Kv, Vv = st["K"], st["V"]
+    sV = None
+    if st["scales"] is not None:
+        sc = np.repeat(st["scales"], plain.BLOCK, axis=1)
+        Kv, Vv, sV = Kv * sc[:, :, 0, :, None], Vv * sc[:, :, 1, :, None], sc[:, :, 1]
+    some = np.arange(min(Nq, 13))
+    ro, ra, rz, rl = plain.attend(Kv, Vv, st["table"], Q[:, some].float().double().numpy(),
+                                  idx[:, some], cnt[:, some], 1 / np.sqrt(d), sV)
+    ra, floor = ra if sV is not None else (ra, 0.0)
+    dz = 2.0 ** -18 * rz
+    tol = 2.0 ** -8 * np.abs(ro) + (2.0 ** -10 + 4 * dz)[..., None] * ra + 2.0 ** -31 * floor + 1e-38
+    skip = np.zeros(ro.shape, bool)
+    rows = hit[:, some].numpy()
+    if which == "K":
+        skip[:, :, 4:] = rows[..., None, None]
+    else:
+        skip[:, :, 4:, 9] = rows[..., None]
+    go = O[:, some].double().numpy()
+    assert (np.abs(go - ro) <= tol)[~skip].all()
+    gl = l[:, some].double().numpy()
+    ok = ~np.isneginf(rl) & ~(skip.all(-1))
+    assert (np.abs(gl[ok] - rl[ok]) <= (2 * dz + 2.0 ** -19 * (1 + np.abs(rl)))[ok]).all()
+    assert np.array_equal(np.isneginf(gl), np.isneginf(rl))
+
+
+@pytest.mark.parametrize("B,Nq,s", SPLITS)
+def test_attention_logits_past_the_range_of_fp32(B, Nq, s):
+    # logits that only the scale takes past the range: -inf beside others weighs nothing, and a row
+    # of nothing else is no empty row
+    rng = np.random.default_rng(107)
+    Hq, Hkv, d, page, mp = 4, 1, 64, 16, 8
+    c = _cache(rng, B, Hkv, d, page, mp, torch.bfloat16)
+    c.k_pages.zero_()
+    far = c.page_table[:, 0].long()
+    c.k_pages[far] = 1e18                               # positions 0 .. 15: products of -6.4e36
+    Q = torch.full((B, Nq, Hq, d), -1e17, dtype=torch.bfloat16)
+    idx, cnt = _rows(rng, B, Nq, mp * page - page, s, [s, 1, s, 17])
+    idx[idx >= 0] += page                               # of the other pages: logits of 0
+    v = c.v_pages.float().cpu()
+    idx[0, 0, 3], idx[0, 0, s - 1] = 4, 11              # two far ones in a full row
+    idx[0, 1, 0] = 7                                    # a far one alone
+    O, l = lsa.lsa_paged_attn(c, Q.cuda(), torch.from_numpy(idx).cuda(), torch.from_numpy(cnt).cuda(),
+                              scale=1e4, return_lse=True)
+    c.check()
+    assert torch.isnan(O[0, 1]).all() and torch.isneginf(l[0, 1]).all()
+    table = c.page_table.cpu().numpy()
+    t = np.delete(idx[0, 0, :s], [3, s - 1])
+    want = v[table[0, t // page], t % page, 0].double().mean(0)
+    size = v[table[0, t // page], t % page, 0].double().abs().mean(0)
+    got = O[0, 0].cpu().double()
+    assert ((got - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -10 * size).all()
+    assert ((l[0, 0].cpu().double() - np.log(len(t))).abs() <= 2.0 ** -19 * (1 + np.log(len(t)))).all()
