@@ -186,3 +186,53 @@ def test_attention_logits_past_the_range_of_fp32(B, Nq, s):
     got = O[0, 0].cpu().double()
     assert ((got - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -10 * size).all()
     assert ((l[0, 0].cpu().double() - np.log(len(t))).abs() <= 2.0 ** -19 * (1 + np.log(len(t)))).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, FP8])
+@pytest.mark.parametrize("inter", [False, True])
+def test_append_rotates_keys_and_queries_that_are_not_finite(dtype, inter):
+    # an infinity's pair becomes infinities (or NaN at position 0, where it meets a sine of 0);
+    # the scale is that of the largest finite rotated magnitude of the block, infinities take the
+    # largest code
+    rng = np.random.default_rng(109)
+    B, Nq, Hq, Hkv, d, page = 2, 21, 4, 2, 64, 16
+    c = lsa.LsaPagedKV.empty(B, 9, page, 4, Hkv, d, dtype)
+    c.page_table.copy_(torch.tensor([[4, 0, 2, 6], [1, 5, 3, 7]], dtype=torch.int32))
+    k, q = _new(rng, B, Nq, Hkv, d), _new(rng, B, Nq, Hq, d)
+    inf, nan = float("inf"), float("nan")
+    for x in (k, q):
+        x[0, 0, 0, 3] = inf                             # position 0
+        x[0, 5, 1, 9], x[0, 6, 1, 40], x[0, 7, 1, 2] = inf, -inf, nan
+        x[1, 3, 0, 10], x[1, 3, 0, 11], x[1, 3, 0, 42] = inf, -inf, inf
+        x[1, 20, 1] = inf                               # a whole row, alone in its block
+    v = _new(rng, B, Nq, Hkv, d)
+    start = np.array([0, 12], np.int32)
+    inv = _freq(d)
+    before = _state(c)
+    out = lsa.lsa_paged_append(c, k.cuda(), v.cuda(), torch.from_numpy(start).cuda(), q=q.cuda(),
+                               inv_freq=torch.from_numpy(inv).cuda(), interleaved=inter)
+    c.check()
+    want = {n: (None if x is None else x.copy()) for n, x in before.items()}
+    with np.errstate(invalid="ignore"):
+        wq = plain.append(want, k.float().double().numpy(), v.float().double().numpy(), start, [Nq] * B,
+                          inv, inter, q.float().double().numpy())
+    g = out.float().cpu().double().numpy()
+    assert np.array_equal(np.isnan(g), np.isnan(wq)) and np.array_equal(np.isinf(g), np.isinf(wq))
+    assert np.array_equal(np.sign(g)[np.isinf(g)], np.sign(wq)[np.isinf(g)])
+    got = _state(c)
+    assert np.array_equal(np.isnan(got["K"]), np.isnan(want["K"]))
+    if dtype == FP8:
+        # no largest magnitude is so near a border of the scale that the rotation's error (2^-21
+        # of the pair) passes it; a code may fall on the other side of a half way: one step
+        for pg in np.argwhere(want["scales"] > 0)[:, 0]:
+            assert np.array_equal(got["scales"][pg], want["scales"][pg])
+        top = np.abs(want["K"]) == 448
+        assert np.array_equal(got["K"][top], want["K"][top])
+        step = plain.half_step(np.nan_to_num(want["K"]))
+        near = np.abs(got["K"] - want["K"]) <= 2 * step * 1.0001 + 1e-12
+        assert (near | np.isnan(want["K"])).all()
+    else:
+        assert np.array_equal(np.isinf(got["K"]), np.isinf(want["K"]))
+        fin = np.isfinite(want["K"])
+        pair = 2.0 ** -21 * 2 * np.nanmax(np.abs(k.float().numpy())[np.isfinite(k.float().numpy())])
+        assert (np.abs(got["K"][fin] - want["K"][fin]) <= 2.0 ** -8 * np.abs(want["K"])[fin] + pair).all()
