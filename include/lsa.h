@@ -628,7 +628,7 @@ lsa_status lsa_paged_append(const lsa_paged_kv* kv, const void* k, int64_t k_str
  * that lists no key gets O = 0 and lse = -inf; a listed position outside [0, max_pages * page), or
  * on a page outside [0, n_pages), is skipped and recorded in the status.  lse
  * (nullable) [B][Nq][Hq] f32: max + ln(sum) of the scaled logits.  For 8-bit
- * pages the scales may be any positive numbers.  Asynchronous on `stream`,
+ * pages the scales may be any positive normal numbers.  Asynchronous on `stream`,
  * graph-capturable, no workspace.  Slots that no row lists are never read.  An
  * infinity or NaN in a listed row, or in Q, makes the results that it enters
  * non-finite (NaN where exact arithmetic may give an infinity): in a key or in Q

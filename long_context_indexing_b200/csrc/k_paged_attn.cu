@@ -404,7 +404,7 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
                 if (E4M3) {
                     const float* s = scale_s + (it & 1) * 64 + half * 16 + u * 8 + r8;
                     kf[u] *= s[0];
-                    ev[u] = __log2f(fmaxf(s[32], 1e-37f));
+                    ev[u] = __log2f(fmaxf(s[32], 1.17549435e-38f));   // (the least normal)
                 }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -572,6 +572,9 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
 #pragma unroll
         for (int i = 0; i < C::EPT; ++i) o[i] += f * src[i * 64];
     }
+    // What takes a sum of weighted values from the reference m2 to m1, in two equal factors:
+    // the scales of values alone reach from 2^-126 to 2^127, so that one would be flushed.
+    auto lift = [](float x) { return E4M3 ? ex2(0.5f * x) : 1.f; };
     if (n_cta > 1) {
         asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
         // thread t's elements go to CTA t / tpc, place (source CTA, t % tpc)
@@ -589,13 +592,14 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
     }
     if (n_cta == 1) {
         const bool empty = M1 == PT_EMPTY;
-        const float f = ex2(M2 - M1) / L;
+        const float f = 1.f / L, e = lift(M2 - M1);
         if (h < nh) {
             __nv_bfloat16* dst = a.O + (hbase + h) * D + dim;
             uint32_t w[C::EPT / 2];
 #pragma unroll
             for (int i = 0; i < C::EPT / 2; ++i)
-                w[i] = ptx::pack_bf16(empty ? 0.f : o[2 * i] * f, empty ? 0.f : o[2 * i + 1] * f);
+                w[i] = ptx::pack_bf16(empty ? 0.f : o[2 * i] * f * e * e,
+                                      empty ? 0.f : o[2 * i + 1] * f * e * e);
             if (C::EPT == 8) *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
             else *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
             if (a.lse && dim == 0)
@@ -625,7 +629,8 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
         }
         if (hh < nh) {
             const bool empty = N1 == PT_EMPTY;
-            a.O[(hbase + hh) * D + dd] = __float2bfloat16_rn(empty ? 0.f : v * (ex2(N2 - N1) / S));
+            const float e = lift(N2 - N1);
+            a.O[(hbase + hh) * D + dd] = __float2bfloat16_rn(empty ? 0.f : v / S * e * e);
             if (a.lse && dd == 0)
                 a.lse[hbase + hh] = empty ? -INFINITY : (N1 + log2f(S)) * 0.6931471805599453f;
         }

@@ -236,3 +236,38 @@ def test_append_rotates_keys_and_queries_that_are_not_finite(dtype, inter):
         fin = np.isfinite(want["K"])
         pair = 2.0 ** -21 * 2 * np.nanmax(np.abs(k.float().numpy())[np.isfinite(k.float().numpy())])
         assert (np.abs(got["K"][fin] - want["K"][fin]) <= 2.0 ** -8 * np.abs(want["K"])[fin] + pair).all()
+
+
+@pytest.mark.parametrize("B,Nq,s", SPLITS)
+@pytest.mark.parametrize("q_exp,k_exp,v_exp", [(1, -6, -126), (1, -6, -100), (1, -6, 117),
+                                               (110, -115, -64), (-110, 105, 0), (1, -126, -126)])
+def test_attention_with_scales_at_the_ends_of_their_range(q_exp, k_exp, v_exp, B, Nq, s):
+    # scales from the least normal number to where the values leave bf16's range, the queries such
+    # that the logits stay in theirs; factors of up to 2 between blocks
+    rng = np.random.default_rng(113)
+    Hq, Hkv, d, page, mp = 8, 2, 64, 16, 12
+    c = _cache(rng, B, Hkv, d, page, mp, FP8)
+    sc = rng.uniform(1.0, 2.0, c.scales.shape)
+    sc[:, :, 0] *= 2.0 ** k_exp
+    sc[:, :, 1] *= 2.0 ** v_exp
+    c.scales.copy_(torch.from_numpy(sc.astype(np.float32)))
+    idx, cnt = _rows(rng, B, Nq, mp * page, s, [s, 1, 40, 0, 17])
+    Q = torch.from_numpy(rng.standard_normal((B, Nq, Hq, d)) * 2.0 ** q_exp).to(torch.bfloat16)
+    O, l = lsa.lsa_paged_attn(c, Q.cuda(), torch.from_numpy(idx).cuda(), torch.from_numpy(cnt).cuda(),
+                              return_lse=True)
+    c.check()
+    some = np.arange(min(Nq, 12))
+    st = _state(c)
+    sv = np.repeat(st["scales"], plain.BLOCK, axis=1)
+    ro, (ra, floor), rz, rl = plain.attend(
+        st["K"] * sv[:, :, 0, :, None], st["V"] * sv[:, :, 1, :, None], st["table"],
+        Q[:, some].float().double().numpy(), idx[:, some], cnt[:, some], 1 / np.sqrt(d), sv[:, :, 1])
+    dz = 2.0 ** -18 * rz
+    # (bf16's subnormals: half of 2^-133)
+    tol = 2.0 ** -8 * np.abs(ro) + (2.0 ** -10 + 4 * dz)[..., None] * ra + 2.0 ** -31 * floor + 2.0 ** -134
+    go = O[:, some].float().cpu().double().numpy()
+    assert (np.abs(go - ro) <= tol).all(), np.max(np.abs(go - ro) / tol)
+    gl = l[:, some].cpu().double().numpy()
+    empty = np.isneginf(rl)
+    assert np.array_equal(np.isneginf(gl), empty)
+    assert (np.abs(gl[~empty] - rl[~empty]) <= (2 * dz + 2.0 ** -19 * (1 + np.abs(rl)))[~empty]).all()
