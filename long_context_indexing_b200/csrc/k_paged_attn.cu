@@ -51,6 +51,7 @@
 // 16-key stage of 8-bit rows issues about 285 instructions, 135 of them on the ALU
 // pipe (64 conversions), at 55 to 60 % of the issue slots; CTAs of 8 warps, stages
 // of 32 keys and L2 prefetches of later tiles were no faster.
+#include <atomic>
 #include <type_traits>
 
 #include "paged.cuh"
@@ -637,6 +638,45 @@ paged_attn_kernel(lsa_paged_kv kv, PagedAttnArgs a)
     }
 }
 
+// Clusters of c CTAs (2, 4, 8, 16) that the current device holds at once; 0 where it takes
+// none.  What its GPCs have room for, which is less than its SMs' places: 31 of 16 with four
+// CTAs on an SM, 21 with three.  Asked once per device.
+template <bool E4M3, int D>
+int cluster_room(int c)
+{
+    constexpr int MAXDEV = 64;
+    static std::atomic<int> known[MAXDEV][PT_MAX_C + 1];   // one more than the answer
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (dev < MAXDEV) {
+        const int k = known[dev][c].load(std::memory_order_relaxed);
+        if (k > 0) return k - 1;
+    }
+    const auto kern = paged_attn_kernel<E4M3, D>;
+    cudaError_t e = ensure_smem_attr((const void*)kern, PagedCfg<E4M3, D>::BYTES);
+    if (e == cudaSuccess && c > 8)
+        e = cudaFuncSetAttribute((const void*)kern,
+                                 cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)c);
+    cfg.blockDim = dim3(PT_THREADS);
+    cfg.dynamicSmemBytes = PagedCfg<E4M3, D>::BYTES;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = (unsigned)c;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        n = 0;
+    }
+    if (dev < MAXDEV) known[dev][c].store(n + 1, std::memory_order_relaxed);
+    return n;
+}
+
 cudaError_t launch_paged_attn(const lsa_paged_kv& kv, const void* Q, int64_t Nq, int Hq,
                               const int32_t* indices, const int32_t* counts, int s_max,
                               float scale, void* O, float* lse, cudaStream_t st)
@@ -664,15 +704,15 @@ cudaError_t launch_paged_attn(const lsa_paged_kv& kv, const void* Q, int64_t Nq,
     // choice, where splits that fill half of the places were 4 % behind it (40 units of
     // 4,612 keys: 4 CTAs 18.9 us, 8 16.4; 128 units of 260 keys: one 6.3, two 8.8).
     // Clusters never fill the last places (148 units of 3,016 keys: 26.7 us with two, 35.1
-    // with four, which would just fit), still less a second wave (256 bf16 units: 58.8 us
-    // with one, 75.1 with two); of 16 the GPCs have room for 31 (32 units: 14.6 us with 8,
-    // 22.7 with 16).
-    auto split = [&](int64_t n) {
+    // with four, which the SMs' places would just hold), still less a second wave (256 bf16
+    // units: 58.8 us with one, 75.1 with two; 32 units: 14.6 us with 8, 22.7 with 16, of which
+    // the device holds 31).
+    auto split = [&](int64_t n, auto room) {
         int best = 1;
         int64_t least = 0;
         for (int c = 1; c <= PT_MAX_C; c *= 2) {
             const int64_t ctas = n * c, on_sm = (ctas + sms - 1) / sms;
-            if (c > 1 && (ctas * 20 > slots * 19 || (c == 16 && n > 31))) break;
+            if (c > 1 && (ctas * 20 > slots * 19 || n > room(c))) break;
             const int tiles = (int)(((int64_t)s_max + 32 * PT_WARPS * c - 1) / (32 * PT_WARPS * c));
             const int64_t merge = c == 1 ? 0 : c == 2 ? 22 : c < 16 ? 18 : 27;
             const int64_t cost = tiles * (10 + (on_sm < 4 ? on_sm : 4)) + merge * on_sm;
@@ -697,16 +737,11 @@ cudaError_t launch_paged_attn(const lsa_paged_kv& kv, const void* Q, int64_t Nq,
     // 76), but only the device knows their counts.
     const int64_t rest = units > slots && units < 3 * slots && s_max >= 1024 ? units % slots : 0;
     const int64_t behind = rest <= slots * 3 / 8 ? rest : 0;
-    auto run = [&](auto kern, int bytes) {
+    auto run = [&](auto kern, int bytes, auto room) {
         cudaError_t e = ensure_smem_attr((const void*)kern, bytes);
         if (e != cudaSuccess) return e;
         auto launch = [&](int64_t n) {
-            const int c = split(n);
-            if (c > 8) {
-                e = cudaFuncSetAttribute((const void*)kern,
-                                         cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-                if (e != cudaSuccess) return e;
-            }
+            const int c = split(n, room);
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3((unsigned)(n * c));
             cfg.blockDim = dim3(PT_THREADS);
@@ -730,11 +765,15 @@ cudaError_t launch_paged_attn(const lsa_paged_kv& kv, const void* Q, int64_t Nq,
     };
     cudaError_t e;
     if (kv.format == LSA_KV_E4M3)
-        e = kv.d == 64 ? run(paged_attn_kernel<true, 64>, PagedCfg<true, 64>::BYTES)
-                       : run(paged_attn_kernel<true, 128>, PagedCfg<true, 128>::BYTES);
+        e = kv.d == 64 ? run(paged_attn_kernel<true, 64>, PagedCfg<true, 64>::BYTES,
+                             cluster_room<true, 64>)
+                       : run(paged_attn_kernel<true, 128>, PagedCfg<true, 128>::BYTES,
+                             cluster_room<true, 128>);
     else
-        e = kv.d == 64 ? run(paged_attn_kernel<false, 64>, PagedCfg<false, 64>::BYTES)
-                       : run(paged_attn_kernel<false, 128>, PagedCfg<false, 128>::BYTES);
+        e = kv.d == 64 ? run(paged_attn_kernel<false, 64>, PagedCfg<false, 64>::BYTES,
+                             cluster_room<false, 64>)
+                       : run(paged_attn_kernel<false, 128>, PagedCfg<false, 128>::BYTES,
+                             cluster_room<false, 128>);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -271,3 +271,59 @@ def test_attention_with_scales_at_the_ends_of_their_range(q_exp, k_exp, v_exp, B
     empty = np.isneginf(rl)
     assert np.array_equal(np.isneginf(gl), empty)
     assert (np.abs(gl[~empty] - rl[~empty]) <= (2 * dz + 2.0 ** -19 * (1 + np.abs(rl)))[~empty]).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, FP8])
+@pytest.mark.parametrize("rows", [1, 10, 11, 15, 16, 24, 25, 26, 35, 36, 52, 53, 71, 75])
+def test_attention_of_as_many_rows_as_clusters_fit(dtype, rows):
+    # two units to a row: up to and past the clusters of 16, 8, 4 and 2 CTAs that a device holds at
+    # once (21, 48, 104, 222 or 31, 71, 142, 296 by the CTAs on an SM), each row whole
+    rng = np.random.default_rng(127)
+    Hq, Hkv, d, page, mp, s = 6, 2, 128, 32, 4, 2100
+    c = _cache(rng, rows, Hkv, d, page, mp, dtype)
+    idx, cnt = _rows(rng, rows, 1, mp * page, s, [s, s - 1, s - 33])
+    Q = _new(rng, rows, 1, Hq, d).cuda()
+    O, l = lsa.lsa_paged_attn(c, Q, torch.from_numpy(idx).cuda(), torch.from_numpy(cnt).cuda(),
+                              return_lse=True)
+    c.check()
+    _check_attn(c, Q, idx, cnt, d ** -0.5, O, l)
+
+
+_FIRST_CALLS = '''
+import sys, torch
+sys.path.insert(0, sys.argv[1])
+import long_context_indexing_b200 as lsa
+FP8 = torch.float8_e4m3fn
+out = []
+with torch.no_grad():
+    c = lsa.LsaPagedKV.empty(3, 12, 64, 4, 2, 128, FP8)
+    c.page_table.copy_(torch.arange(12, dtype=torch.int32).view(3, 4))
+    g0 = torch.Generator().manual_seed(5)
+    k = torch.randn(3, 200, 2, 128, generator=g0).bfloat16().cuda()
+    q = torch.randn(3, 200, 8, 128, generator=g0).bfloat16().cuda()
+    start = torch.zeros(3, dtype=torch.int32, device="cuda")
+    idx = torch.randint(0, 200, (3, 1, 150), generator=g0, dtype=torch.int32).cuda()
+    cnt = torch.full((3, 1), 150, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        qr = lsa.lsa_paged_append(c, k, k, start, q=q)
+        O = lsa.lsa_paged_attn(c, q[:, :1].contiguous(), idx, cnt)
+    g.replay()
+    torch.cuda.synchronize()
+    P = lsa.lsa_paged_attn(c, q[:, :1].contiguous(), idx, cnt)
+    assert torch.equal(O, P) and O.float().abs().max() > 0
+    c.check()
+print("same")
+'''
+
+
+def test_first_calls_of_a_process_captured():
+    # what a call asks of the device once is asked inside the capture
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", _FIRST_CALLS, root], capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
