@@ -595,9 +595,9 @@ typedef struct {
  *   q        bf16 rows of Hq * d at q_stride, or NULL; q_out [B][Nq][Hq][d]
  *            receives them rotated (q_out == q is allowed when q is
  *            contiguous); rows of padding are left as they were
- *   inv_freq [rot_dim / 2] f32, finite (NULL when rot_dim is 0: no rotation):
- *            pair j of a head turns by t * inv_freq[j] radians (the product exact
- *            to 2^-31 of a turn, whatever t).  The pairs are (j, j +
+ *   inv_freq [rot_dim / 2] f32 of magnitude up to 2^44 (NULL when rot_dim is 0: no
+ *            rotation): pair j of a head turns by t * inv_freq[j] radians (the
+ *            product exact to 2^-31 of a turn, whatever t).  The pairs are (j, j +
  *            rot_dim/2), or (2j, 2j + 1) when interleaved != 0; elements from
  *            rot_dim on, and V, are not turned.  rot_dim is a multiple of 16
  *            up to d.

@@ -39,8 +39,9 @@ constexpr int PA_THREADS = 256;
 constexpr int PA_WARPS = PA_THREADS / 32;
 
 // f / (2 pi) turns per position as a 64-bit fraction of a turn: a position's turn
-// is then a product modulo 2^64, exact but for f's own rounding (2^-63, so 2^-32
-// of a turn at the last position).
+// is then a product modulo 2^64, exact but for f's own rounding (2^-63 for |f| up to
+// 2^44, so 2^-32 of a turn at the last position; past 2^53 the quotient's low part has
+// whole turns and no fraction is left).
 __device__ __forceinline__ uint64_t turns_of(float f)
 {
     constexpr double INV = 0.15915494309189535, INV_LO = -9.839338337591243e-18;   // 1 / (2 pi)

@@ -327,3 +327,44 @@ def test_first_calls_of_a_process_captured():
     r = subprocess.run([sys.executable, "-c", _FIRST_CALLS, root], capture_output=True, text=True,
                        timeout=300)
     assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
+
+
+def test_append_turns_by_large_frequencies_at_far_positions():
+    # the angle's product to 2^-31 of a turn for every frequency up to 2^44: against exact
+    # fractions of a turn (1 / (2 pi) to 400 bits by Machin's formula)
+    from fractions import Fraction
+
+    def arctan_inv(x):
+        t = (1 << 420) // x
+        s, n, sign = t, 3, -1
+        while t:
+            t //= x * x
+            s, n, sign = s + sign * (t // n), n + 2, -sign
+        return s
+
+    inv_2pi = Fraction(1 << 420, 8 * (4 * arctan_inv(5) - arctan_inv(239)))
+    rng = np.random.default_rng(131)
+    d, page, rot = 64, 1024, 64
+    inv = (2.0 ** rng.uniform(-30, 44, rot // 2)).astype(np.float32) * rng.choice([-1, 1], rot // 2)
+    inv = inv.astype(np.float32)
+    inv[:4] = [2.0 ** 44, -(2.0 ** 44), 0.0, 2.0 ** 44 * (1 - 2.0 ** -24)]
+    at = np.array([0, 1, 10485759, 2 ** 31 - 1025], np.int32)
+    B = len(at)
+    table = torch.full((B, (2 ** 31 - 1) // page), -1, dtype=torch.int32, device="cuda")
+    for b in range(B):
+        table[b, at[b] // page] = b
+    pages = torch.zeros(B, page, 1, d, dtype=torch.bfloat16, device="cuda")
+    c = lsa.LsaPagedKV(pages, pages.clone(), table)
+    k = _new(rng, B, 1, 1, d)
+    q = _new(rng, B, 1, 2, d)
+    out = lsa.lsa_paged_append(c, k.cuda(), k.cuda(), torch.from_numpy(at).cuda(), q=q.cuda(),
+                               inv_freq=torch.from_numpy(inv).cuda())
+    c.check()
+    for b in range(B):
+        a = np.array([float((int(at[b]) * Fraction(float(f)) * inv_2pi) % 1) for f in inv]) * 2 * np.pi
+        for x, y in ((q[b, 0], out[b, 0]), (k[b, 0], c.k_pages[b, at[b] % page])):
+            x, y = x.float().double().numpy(), y.float().cpu().double().numpy()
+            u, v = x[:, :rot // 2], x[:, rot // 2:]
+            want = np.concatenate([u * np.cos(a) - v * np.sin(a), v * np.cos(a) + u * np.sin(a)], 1)
+            pair = np.tile(np.abs(u) + np.abs(v), 2)
+            assert (np.abs(y - want) <= 2.0 ** -8 * np.abs(want) + 1.01 * 2.0 ** -21 * pair).all()
