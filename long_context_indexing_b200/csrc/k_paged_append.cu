@@ -25,8 +25,8 @@
 // leaves the registers to three CTAs per SM: with four CTAs the queries' part spills
 // (heads of 64: padded batch 12.1 us against 11.7; 32,768 tokens 53 against 55), with
 // two the keys' part waits (32,768 tokens of 4 heads 45 us against 38).
-// Measured (B200): 32,768 tokens of 32/4 heads of 128 into 8-bit pages 102 us (637.6
-// MB, 6.25 TB/s, 0.95 of a copy's rate: HBM); 2 x 4,096 tokens of 16/2 heads into
+// Measured (B200): 32,768 tokens of 32/4 heads of 128 into 8-bit pages 101 us (637.6
+// MB, 6.3 TB/s, 0.96 of a copy's rate: HBM); 2 x 4,096 tokens of 16/2 heads into
 // bf16 pages 16.2 us (5.2 TB/s; 514 blocks, the queries in CTAs of their own); 7 padded
 // prompts of up to 1,021 tokens of 24/8 heads of 64 10 us (waves of latencies:
 // start 1.0 us, page and turns 2, keys and values 3.6, queries 2.8); 256 tokens of 32/4 heads 4.2 us, 8 tokens 3.1.

@@ -27,9 +27,11 @@
 //     (what falls below f16's subnormals is 2^-37 of their largest element).  sK
 //     multiplies the logit in fp32; sV joins the exponent of the weight, w_t =
 //     2^(z_t + log2 sV_t - m2), so that the f16 weight of the largest
-//     contribution is from 2^7 to 2^15 whatever the scales: 2^-11 relative, down
-//     to 2^-32 of the largest.  The denominator sums 2^(z_t - m1) in fp32 with a
-//     reference of its own.
+//     contribution is from 2^7 to 2^15 whatever the scales: a weight is off by
+//     2^-11 of itself or, below f16's normal range, by 2^-32 of the largest.  (An
+//     eighth of the output's own rounding to bf16 at most; a second f16 for the
+//     rest would double the products with V.)  The denominator sums 2^(z_t - m1)
+//     in fp32 with a reference of its own.
 //   * bf16 pages: the weight as the sum of two bf16 (2^-17 relative), since one
 //     would add as much error as the output's rounding.
 //   * The references m1, m2 move only when a value passes them by 2^15: one vote
@@ -41,13 +43,17 @@
 // then send each other the slice that the other finishes (distributed shared
 // memory, one barrier).
 //
+// A row is empty when no warp met a key with a slot (PT_EMPTY), whatever its sum; z
+// times 0 joins the sum so that infinities and NaN of Q or K are not lost with a weight
+// of 0.  All of that is under 1 % of a call.
+//
 // Bound and measured (B200, 32/4 heads of 128 unless said): 8 rows of 4,612 keys,
-// 8-bit, 13.5 us, of which 3.6 before the first product (positions, pages, rows:
+// 8-bit, 13.6 us, of which 3.6 before the first product (positions, pages, rows:
 // three dependent reads) and 3 in the merge; 32 rows 33 us (4.6 TB/s); 64 rows of
 // 16/2 heads in bf16 pages 52 us (5.8 TB/s, 0.89 of a copy's rate: HBM); 251 rows
-// of 16/2 heads over 128k in bf16 pages 104 to 113 us (10.5 to 11.4 TB/s of rows, most
-// of them from L2); 1,024 rows of 2,564 keys over 1M, 8-bit, 394 to 417 us (6.5 to 6.8
-// TB/s of rows: HBM, for rows that list the same bucket seldom run together).  With all warps busy a
+// of 16/2 heads over 128k in bf16 pages 109 to 117 us by the card (10.1 to 10.9 TB/s of
+// rows, most of them from L2); 1,024 rows of 2,564 keys over 1M, 8-bit, 388 to 417 us (6.5
+// to 7.0 TB/s of rows: HBM, for rows that list the same bucket seldom run together).  With all warps busy a
 // 16-key stage of 8-bit rows issues about 285 instructions, 135 of them on the ALU
 // pipe (64 conversions), at 55 to 60 % of the issue slots; CTAs of 8 warps, stages
 // of 32 keys and L2 prefetches of later tiles were no faster.
@@ -698,7 +704,8 @@ cudaError_t launch_paged_attn(const lsa_paged_kv& kv, const void* Q, int64_t Nq,
     const int64_t units = kv.B * Nq * kv.Hkv * a.chunks;
     const int64_t sms = sm_count(), slots = sms * (kv.format == LSA_KV_BF16 && kv.d == 128 ? 3 : 4);
     // CTAs per unit: those of the least cost by what was measured of 686 calls (2 to 512
-    // units of 100 to 8,708 keys, heads of 64 and 128, both formats), in tenths of a tile's
+    // units of 100 to 8,708 keys, heads of 64 and 128, both formats; the times are in
+    // profiles/paged_split.csv), in tenths of a tile's
     // time: a warp's tiles, each dearer by a tenth for every CTA on the SM, and the merge
     // between CTAs, for every one on the SM.  On the mean it is within 1 % of the best
     // choice, where splits that fill half of the places were 4 % behind it (40 units of
