@@ -624,17 +624,19 @@ lsa_status lsa_paged_append(const lsa_paged_kv* kv, const void* k, int64_t k_str
 
 /* lsa_sparse_attn over the paged cache: Q, O [B][Nq][Hq][d] bf16, indices
  * [B][Nq][s_max] positions (as the selections write them; s_max up to 2^30),
- * counts [B][Nq].  fp32 softmax and accumulation; Hq a multiple of Hkv.  A row
- * that lists no key gets O = 0 and lse = -inf; a listed position outside [0, max_pages * page), or
- * on a page outside [0, n_pages), is skipped and recorded in the status.  lse
- * (nullable) [B][Nq][Hq] f32: max + ln(sum) of the scaled logits.  For 8-bit
- * pages the scales may be any positive normal numbers.  Asynchronous on `stream`,
- * graph-capturable, no workspace.  Slots that no row lists are never read.  An
- * infinity or NaN in a listed row, or in Q, makes the results that it enters
+ * counts [B][Nq].  Logits, the softmax's maximum and sum, and accumulation in
+ * fp32; the weights that multiply V are rounded to f16 for 8-bit pages (2^-11
+ * relative) and to two bf16 for bf16 pages (2^-17).  Hq a multiple of Hkv.  A row
+ * that lists no key gets O = 0 and lse = -inf; a listed position outside
+ * [0, max_pages * page), or on a page outside [0, n_pages), is skipped and recorded
+ * in the status.  lse (nullable) [B][Nq][Hq] f32: max + ln(sum) of the scaled
+ * logits.  For 8-bit pages the scales may be any positive normal numbers.
+ * Asynchronous on `stream`, graph-capturable, no workspace.  Slots that no row
+ * lists are never read.  An infinity or NaN in a listed row, or in Q, makes the results that it enters
  * non-finite (NaN where exact arithmetic may give an infinity): in a key or in Q
  * those of the head, lse too (NaN), in a value those of its element.  So does a
  * product of a query and a key that passes fp32's range; a logit that does so only
- * by the scale weighs nothing beside others, and gives NaN alone. */
+ * by the scale weighs nothing beside others, and alone gives O = NaN, lse = -inf. */
 lsa_status lsa_paged_attn(const lsa_paged_kv* kv, const void* Q, int64_t Nq, int Hq,
                           const int32_t* indices, const int32_t* counts, int s_max, float scale,
                           void* O, float* lse, void* stream);

@@ -29,9 +29,10 @@
 //     2^(z_t + log2 sV_t - m2), so that the f16 weight of the largest
 //     contribution is from 2^7 to 2^15 whatever the scales: a weight is off by
 //     2^-11 of itself or, below f16's normal range, by 2^-32 of the largest.  (An
-//     eighth of the output's own rounding to bf16 at most; a second f16 for the
-//     rest would double the products with V.)  The denominator sums 2^(z_t - m1)
-//     in fp32 with a reference of its own.
+//     eighth of the output's own rounding to bf16 at most: the mean error against
+//     64 bits is 1.0006 times that of fp32 weights.  A second f16 for the rest costs
+//     3 to 10 %: 8 rows 14.1 us against 14.9, 1,024 rows 370 against 403.)  The
+//     denominator sums 2^(z_t - m1) in fp32 with a reference of its own.
 //   * bf16 pages: the weight as the sum of two bf16 (2^-17 relative), since one
 //     would add as much error as the output's rounding.
 //   * The references m1, m2 move only when a value passes them by 2^15: one vote
