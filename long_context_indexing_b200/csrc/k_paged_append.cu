@@ -256,6 +256,7 @@ __global__ void __launch_bounds__(PA_THREADS, 3) paged_append_kernel(lsa_paged_k
     };
 
     // ---- keys and values ----
+    if (pg < 0) ptx::cp_async_wait<0>();     // (what was asked for is not used)
     const int64_t slot0 = (int64_t)pg * kv.page + (p0 & (kv.page - 1));
     int at = 0;
     for (int it = warp; it < 2 * Hkv && do_kv && pg >= 0; it += PA_WARPS) {
